@@ -295,7 +295,7 @@ def _handles(s):
     from host_streamed_paged_kvs_b200 import kvs
     c = s["case"]
     h = dict(kvs=kvs, pool=kvs.make_page_pool(s["pool"], c["n_kv"], c["type_k"], c["type_v"]),
-             batch=kvs.make_page_batch(s["start"], s["lens"], s["table"], s["rows"]))
+             batch=kvs.make_page_batch(s["start"], s["lens"], s["table"], s["rows"], max_new=max(_lengths(c)[0])))
     if c["op"] == "append":
         h["rope"] = kvs.make_rope(s["inv_freq"], c["rot"], interleaved=c["inter"])
     if c["op"] == "attend":
