@@ -9,8 +9,9 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libkvs.so")
-SOURCES = ["kvs_kernels.cu", "kvs_chunk_mma.cu", "kvs_runtime.cpp", "kvs_static.cu"]
-HEADERS = ["kvs_internal.h", "kvs_ptx.cuh"]
+SOURCES = ["kvs_kernels.cu", "kvs_chunk_mma.cu", "kvs_runtime.cpp", "kvs_static.cu",
+           "kvs_pages.cpp", "kvs_pages.cu", "kvs_pages_few.cu"]
+HEADERS = ["kvs_internal.h", "kvs_ptx.cuh", "kvs_pages.h", "kvs_pages_finish.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 
@@ -31,6 +32,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
+           "--threads", "0",
            "-Xcompiler", "-fPIC,-O2", "-shared", "-I", os.path.join(ROOT, "include"),
            "-o", tmp] + [os.path.join(CSRC, s) for s in SOURCES]
     if verbose:

@@ -1,0 +1,914 @@
+// kvs_pages_few.cu -- attention of few rows per kv head over quantized pages
+// found through page tables (kvs_attend_pages: decode and verify steps, and a
+// shared prefix seen by few rows).
+//
+//   out = sum_j p_j v_j / sum_j p_j,  p_j = 2^(s_j - r),  s_j = log2(e) score(q.k_j)
+//
+// What bounds it: HBM.  A key costs 208 B per kv head (K Q8_0 / V Q4_0) and is
+// read once for all rows of its kv head; at 6.5 TB/s an SM has 9 cycles per
+// key for everything else.
+//
+// Work split.  A unit is (sequence, kv head, up to 8 NT rows); its keys come
+// in stages of 128.  All units' stages form one list, and every CTA (two per
+// SM where the stages fit) takes an equal run of it, whatever the sequences'
+// lengths: one long sequence spreads over all SMs, and many short ones leave
+// none idle.  Each CTA finds its run from the lengths in device memory itself
+// (a block scan), so there is no planning launch, and a captured graph follows
+// the lengths.  A unit that several CTAs share leaves one record per CTA, and
+// the CTA that arrives last joins them in CTA order (a fixed order: results do
+// not depend on which one that is).
+//
+// One producer warp walks the run: per piece (a unit's part in this CTA) it
+// puts the rows' bounds and Q into shared memory, then keeps the stages' TMA
+// copies in flight.  K rows land with the 128-byte swizzle, 4- and 5-bit V rows
+// with the 64-byte swizzle, so that ldmatrix reads eight rows without bank
+// conflicts.  Four consumer warps take 32 keys of each stage, with a softmax
+// state of their own, and join at the piece's end.
+//
+// Both products keep the keys and dims on the 16-row side of mma.sync
+// m16n8k16 and the query rows on the 8-column side, so no tile row is wasted
+// on a step's few rows, and a converted operand serves all NT column tiles:
+//   S^T [keys x rows] = K [keys x dims] Q^T: int8 codes are exact in fp16; the
+//     fp32 sum of each 32-dim block is multiplied by the key's block scale;
+//   O^T [dims x rows] += V^T [dims x keys] P^T: ldmatrix.trans gives a lane the
+//     codes of two neighbouring keys in one word, which is the operand's pair;
+//     codes are exact, and the weight p d_v (one product in fp16, relative to a
+//     reference 2^6 below the maximum so that small weights stay normal) is
+//     the other operand, turned by movmatrix.  In precise mode its rounding
+//     error goes in as a second term, and the sums are fp32-exact.  Q4_1 and
+//     Q5_1 values d q + m are rounded to fp16 instead (weights p).
+#include <cuda_fp16.h>
+#include <math_constants.h>
+
+#include <algorithm>
+#include <atomic>
+#include <climits>
+
+#include "kvs_pages.h"
+#include "kvs_pages_finish.cuh"
+#include "kvs_ptx.cuh"
+
+namespace kvs {
+namespace {
+
+constexpr int kConsumers = 4;
+constexpr int kThreads = (kConsumers + 1) * 32;
+constexpr int kStageKeys = 128;
+constexpr int kQRow = 288;                         // bytes of a Q row in shared memory: 32 mod 128, so that 4 rows x 32 B are distinct banks
+constexpr int kRedRow = 132;                       // floats of a row in the join buffer
+constexpr int kRedBytes = kConsumers * 8 * kRedRow * 4;
+// Waits are bounded; the bound leaves room for rows recomputed the slow way.
+constexpr uint64_t kWaitNs = 10000000000ull;
+
+// A piece: rows of one unit and the stages of it that this CTA takes.
+template <int ROWS>
+struct Piece {
+    int n_stages;             // < 0: no more pieces
+    int first_stage;          // of the unit's pages
+    int rows, seq, kv_head;
+    int full_from, full_to;   // keys every row sees
+    int n_keys;               // keys that exist
+    int slot;                 // record slot, or -1: the whole unit is here
+    int cta0, n_ctas;         // CTAs that share the unit
+    volatile int bad;         // a page number was outside the pool
+    int token[ROWS], head[ROWS];
+    int pos[ROWS], first[ROWS], end[ROWS];  // in keys of this phase
+    float scale[ROWS], slope[ROWS];
+    alignas(16) uint8_t q[ROWS * kQRow];
+};
+
+template <int VT, int KT, int NT>
+struct Geo {
+    using PG = PageGeom<VT, KT>;
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kOffV = kStageKeys * PG::kKqRow;
+    static constexpr int kOffKd = kOffV + kStageKeys * PG::kVqRow;
+    static constexpr int kOffVh = kOffKd + kStageKeys * PG::kKdRow;
+    static constexpr int kOffVd = kOffVh + kStageKeys * PG::kVhRow;
+    static constexpr int kOffVm = kOffVd + kStageKeys * PG::kVdRow;
+    static constexpr int kBytes = kOffVm + kStageKeys * PG::kVmRow;
+    static constexpr size_t kFixed = 1024 + kRedBytes + 2 * sizeof(Piece<kRows>) + 512;
+    static constexpr int kPerSm = NT <= 2 && 2 * (2 * (size_t)kBytes + kFixed + 1024) <= 233472 ? 2 : 1;
+    static constexpr int kFit = (int)((233472 / kPerSm - 1024 - kFixed) / kBytes);
+    static constexpr int kStages = kFit < 4 ? kFit : 4;
+    static constexpr size_t kOffRed = (size_t)kStages * kBytes;
+    static constexpr size_t kOffPiece = kOffRed + kRedBytes;
+    static constexpr size_t kOffBar = kOffPiece + 2 * sizeof(Piece<kRows>);
+    static constexpr size_t kSmem = 1024 + kOffBar + 512;
+    static_assert(kBytes % 1024 == 0 && kOffV % 1024 == 0, "swizzled tiles need aligned stages");
+    static_assert(kStages >= 2 && kSmem <= 232448 && sizeof(Piece<kRows>) % 16 == 0, "shared memory");
+};
+
+__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+__device__ __forceinline__ uint32_t h2u(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t movm(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tma3(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tma4(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar)) : "memory");
+}
+
+// four int8 codes (biased by 128) as two fp16 pairs: bytes 0, 1 and 2, 3
+__device__ __forceinline__ void s8x4(uint32_t w, uint32_t sel0, uint32_t sel1, uint32_t& lo, uint32_t& hi) {
+    const uint32_t x = w ^ 0x80808080u;
+    const __half2 b = __float2half2_rn(1152.0f);  // 1024 of the exponent trick + 128 of the bias
+    lo = h2u(__hsub2(u2h(__byte_perm(x, 0x64646464u, sel0)), b));
+    hi = h2u(__hsub2(u2h(__byte_perm(x, 0x64646464u, sel1)), b));
+}
+
+// the batch's work as this phase sees it
+struct Seq {
+    int row0, rows;           // first row; rows (tokens)
+    int n_keys;               // keys that exist
+    int stage0;               // first stage any row sees
+    int n_groups;             // row groups
+    long long n_stages;       // stages per unit, at least 1
+};
+template <int ROWS>
+__device__ __forceinline__ Seq seq_of(const AttendPagesArgs& a, int i) {
+    Seq s;
+    const PageBatch& b = a.batch;
+    int keys;
+    if (a.prefix_phase) {
+        s.row0 = 0;
+        s.rows = max(0, min(b.n_rows, b.q_start[b.n_seqs]));
+        keys = a.prefix_len;
+        s.n_keys = keys;
+        s.stage0 = 0;
+    } else {
+        s.row0 = b.q_start[i];
+        s.rows = max(0, b.q_start[i + 1] - s.row0);
+        const long long most = (long long)b.table_stride * kPageTokens;
+        s.n_keys = max(0, b.seq_len[i]);
+        keys = (int)min((long long)s.n_keys, most);
+        s.stage0 = 0;
+        if (a.window > 0 && !a.first_key)  // own keys before the first row's window are nobody's
+            s.stage0 = max(0, min(s.n_keys - s.rows - a.window + 1, keys - 1)) / kStageKeys;
+    }
+    s.n_groups = (int)(((long long)s.rows * a.group + ROWS - 1) / ROWS);
+    s.n_stages = max(1, (keys + kStageKeys - 1) / kStageKeys - s.stage0);
+    return s;
+}
+
+template <int VT, int KT, int NT>
+__global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
+    attend_few_kernel(const __grid_constant__ AttendPagesArgs a, const __grid_constant__ PageMaps maps) {
+    using G = Geo<VT, KT, NT>;
+    using PG = PageGeom<VT, KT>;
+    constexpr int ROWS = G::kRows, kStages = G::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    float* red = reinterpret_cast<float*>(smem + G::kOffRed);
+    Piece<ROWS>* pieces = reinterpret_cast<Piece<ROWS>*>(smem + G::kOffPiece);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::kOffBar);  // [stage] bytes landed
+    uint64_t* empty = full + kStages;                                 // [stage] consumers done
+    uint64_t* p_full = empty + kStages;                               // [piece slot] published
+    uint64_t* p_empty = p_full + 2;                                   // [piece slot] consumers done
+    uint64_t* c_bar = p_empty + 2;                                    // the consumers' own barrier
+    long long* sScan = reinterpret_cast<long long*>(c_bar + 1);       // [kConsumers + 1] warp sums
+    long long* sBase = sScan + 8;                                     // stages before the first sequence
+    int* sSeq = reinterpret_cast<int*>(sBase + 1);                    // first sequence of the run
+    int* sLast = sSeq + 1;                                            // this CTA joins the unit
+    float* sml = reinterpret_cast<float*>(sSeq + 4);                  // [warp][8][2] (reference, sum)
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n_units_of = a.pool.n_kv;
+    const int n_seqs = a.prefix_phase ? 1 : a.batch.n_seqs;
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], kConsumers);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&p_full[s], 1);
+            mbar_init(&p_empty[s], kConsumers);
+        }
+        mbar_init(c_bar, kConsumers);
+        fence_mbar_init();
+        *sSeq = n_seqs;
+    }
+
+    // ---- this CTA's run of the list of all units' stages ----
+    long long total = 0;
+    {
+        long long mine = 0;
+        for (int i = tid; i < n_seqs; i += kThreads) {
+            const Seq s = seq_of<ROWS>(a, i);
+            mine += s.n_stages * s.n_groups * n_units_of;
+        }
+#pragma unroll
+        for (int off = 16; off; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
+        if (lane == 0) sScan[warp] = mine;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) total += sScan[w];
+        __syncthreads();
+    }
+    const long long per = max(1ll, (total + gridDim.x - 1) / gridDim.x);
+    const long long run0 = min(total, per * blockIdx.x), run1 = min(total, run0 + per);
+    if (run0 >= run1) return;
+    {
+        long long before = 0;
+        for (int i0 = 0; i0 < n_seqs && before <= run0; i0 += kThreads) {
+            const int i = i0 + tid;
+            long long cost = 0;
+            if (i < n_seqs) {
+                const Seq s = seq_of<ROWS>(a, i);
+                cost = s.n_stages * s.n_groups * n_units_of;
+            }
+            long long upto = cost;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const long long v = __shfl_up_sync(0xffffffffu, upto, off);
+                if (lane >= off) upto += v;
+            }
+            if (lane == 31) sScan[warp] = upto;
+            __syncthreads();
+            long long all = 0;
+#pragma unroll
+            for (int w = 0; w < kThreads / 32; ++w) {
+                if (w < warp) upto += sScan[w];
+                all += sScan[w];
+            }
+            upto += before;
+            if (upto - cost <= run0 && run0 < upto) {
+                *sSeq = i;
+                *sBase = upto - cost;
+            }
+            before += all;
+            __syncthreads();
+        }
+    }
+
+    if (warp == kConsumers) {
+        // ============================ producer ============================
+        int seq = *sSeq;
+        long long base = *sBase, cur = run0;
+        int issued = 0, n_pieces = 0;
+        bool ok = true;
+        Seq s = seq < n_seqs ? seq_of<ROWS>(a, seq) : Seq{};
+        while (ok) {
+            while (seq < n_seqs && cur < run1 && cur >= base + s.n_stages * s.n_groups * n_units_of) {
+                base += s.n_stages * s.n_groups * n_units_of;
+                ++seq;
+                if (seq < n_seqs) s = seq_of<ROWS>(a, seq);
+            }
+            Piece<ROWS>& p = pieces[n_pieces & 1];
+            if (n_pieces >= 2) ok = mbar_wait_bounded(&p_empty[n_pieces & 1], ((n_pieces >> 1) - 1) & 1, a.batch.status, kWaitNs);
+            if (!ok || cur >= run1 || seq >= n_seqs) {
+                if (lane == 0) p.n_stages = -1;
+                __syncwarp();
+                if (lane == 0) arrive(&p_full[n_pieces & 1]);
+                break;
+            }
+            const long long unit = (cur - base) / s.n_stages;
+            const long long unit0 = base + unit * s.n_stages, unit1 = unit0 + s.n_stages;
+            const long long stop = min(run1, unit1);
+            const int group = (int)(unit / n_units_of), h = (int)(unit % n_units_of);
+            const int rows = min(ROWS, s.rows * a.group - group * ROWS);
+            // bounds of the rows, one lane each
+            int first = INT_MAX, end = 0, pos = 0, token = -1, head = 0;
+            float slope = 0.0f;
+            if (lane < rows) {
+                const int r = group * ROWS + lane;
+                token = s.row0 + r / a.group;
+                head = h * a.group + r % a.group;
+                int of = seq;
+                if ((unsigned)token >= (unsigned)a.batch.n_rows) token = -1;
+                else if (a.prefix_phase) {
+                    of = find_seq_thread(a.batch, token);
+                    if (of < 0) token = -1;
+                }
+                if (token >= 0) {
+                    const RowView v = row_view(a, of, token);
+                    const int shift = a.prefix_phase ? 0 : a.prefix_len;
+                    pos = v.pos - shift;
+                    first = max(v.first - shift, 0);
+                    end = min(v.end - shift, s.n_keys);
+                    if (a.slopes) slope = a.slopes[head];
+                }
+            }
+            const bool sees = first < end;
+            int lo = sees ? first : INT_MAX, hi = sees ? end : 0;
+            int full_from = token >= 0 ? first : 0, full_to = token >= 0 ? end : INT_MAX;
+#pragma unroll
+            for (int off = 16; off; off >>= 1) {
+                lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+                hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+                full_from = max(full_from, __shfl_xor_sync(0xffffffffu, full_from, off));
+                full_to = min(full_to, __shfl_xor_sync(0xffffffffu, full_to, off));
+            }
+            int st0 = s.stage0 + (int)(cur - unit0), st1 = s.stage0 + (int)(stop - unit0);
+            if (lo < hi) {
+                st0 = max(st0, lo / kStageKeys);
+                st1 = min(st1, (hi + kStageKeys - 1) / kStageKeys);
+            } else st1 = st0;
+            if (lane < ROWS) {
+                p.token[lane] = token;
+                p.head[lane] = head;
+                p.pos[lane] = pos;
+                p.first[lane] = first;
+                p.end[lane] = end;
+                p.slope[lane] = slope;
+            }
+            if (lane == 0) {
+                p.n_stages = max(0, st1 - st0);
+                p.first_stage = st0;
+                p.rows = rows;
+                p.seq = seq;
+                p.kv_head = h;
+                p.full_from = full_from;
+                p.full_to = full_to;
+                p.n_keys = s.n_keys;
+                p.slot = (unit0 >= run0 && unit1 <= run1) ? -1 : (unit0 < run0 ? 0 : 1);
+                p.cta0 = (int)(unit0 / per);
+                p.n_ctas = (int)((unit1 - 1) / per) - p.cta0 + 1;
+                // a row that may see keys beyond the page table
+                p.bad = hi > (long long)a.batch.table_stride * kPageTokens && !a.prefix_phase;
+            }
+            // Q: fp16 as it is; bf16 as fp16 after taking each row's power of two
+            // out (exact down to 2^-24 of the row's largest value)
+            const float unit_scale = a.softcap > 0.0f || a.slopes ? a.scale : a.scale * 1.4426950408889634f;
+#pragma unroll 4
+            for (int r = 0; r < ROWS; ++r) {
+                const int tk = __shfl_sync(0xffffffffu, token, r), hd = __shfl_sync(0xffffffffu, head, r);
+                uint2 w = make_uint2(0u, 0u);
+                if (tk >= 0)
+                    w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q.p) + tk * a.q.row + hd * a.q.head + 4 * lane);
+                float sc = unit_scale;
+                if (a.q_dtype == kDtBF16) {
+                    const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
+                    const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
+                    float top = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y)));
+#pragma unroll
+                    for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                    // 2^e with 2^e <= top < 2^(e+1); 1 for zero, subnormal and non-finite rows
+                    const uint32_t ex = (__float_as_uint(top) >> 23) & 0xffu;
+                    const bool plain = ex < 2 || ex > 252;
+                    const float up = plain ? 1.0f : __uint_as_float(ex << 23), down = plain ? 1.0f : __uint_as_float((254u - ex) << 23);
+                    *reinterpret_cast<__half2*>(&w.x) = __floats2half2_rn(x.x * down, x.y * down);
+                    *reinterpret_cast<__half2*>(&w.y) = __floats2half2_rn(y.x * down, y.y * down);
+                    sc *= up;
+                }
+                *reinterpret_cast<uint2*>(p.q + r * kQRow + 8 * lane) = w;
+                if (lane == 0) p.scale[r] = sc;
+            }
+            __syncwarp();
+            if (lane == 0) arrive(&p_full[n_pieces & 1]);
+
+            // ---- the piece's stages ----
+            const int* table = a.prefix_phase ? a.prefix_table : a.batch.table + (size_t)seq * a.batch.table_stride;
+            const int n_table = a.prefix_phase ? (a.prefix_len + kPageTokens - 1) / kPageTokens : a.batch.table_stride;
+            int pages = 0, pages_at = -1;  // 32 page numbers, one a lane
+            for (int st = st0; st < st1; ++st) {
+                const int j = st >> 1;
+                if (pages_at < 0 || j >= pages_at + 32) {
+                    pages_at = j;
+                    pages = j + lane < n_table ? table[j + lane] : -1;
+                }
+                int page = __shfl_sync(0xffffffffu, pages, j - pages_at);
+                const int buf = issued % kStages;
+                if (issued >= kStages &&
+                    !mbar_wait_bounded(&empty[buf], ((issued / kStages) - 1) & 1, a.batch.status, kWaitNs)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    if ((unsigned)page >= (unsigned)a.pool.n_pages) {
+                        page = 0;  // some page: its piece comes out as NaN
+                        p.bad = 1;
+                    }
+                    uint8_t* dst = smem + buf * G::kBytes;
+                    uint64_t* bar = &full[buf];
+                    mbar_expect_tx(bar, G::kBytes);
+                    const int hp = page * a.pool.n_kv + h, t0 = (st & 1) * kStageKeys;
+                    const uint8_t* ph = a.pool.pages + (size_t)hp * PG::kHeadBytes;
+                    if constexpr (KT == kKF16) {
+                        tma4(dst, &maps.k, 0, 0, t0, hp, bar);
+                        tma4(dst + kStageKeys * 128, &maps.k, 0, 1, t0, hp, bar);
+                    } else {
+                        tma3(dst, &maps.k, 0, t0, hp, bar);
+                        bulk_load(dst + G::kOffKd, ph + PG::kOffKd + t0 * PG::kKdRow, kStageKeys * PG::kKdRow, bar);
+                    }
+                    if constexpr (VT == kVF16) {
+                        tma4(dst + G::kOffV, &maps.v, 0, 0, PG::kOffVq / 256 + t0, hp, bar);
+                        tma4(dst + G::kOffV + kStageKeys * 128, &maps.v, 0, 1, PG::kOffVq / 256 + t0, hp, bar);
+                    } else {
+                        tma3(dst + G::kOffV, &maps.v, 0, PG::kOffVq / PG::kVqRow + t0, hp, bar);
+                        bulk_load(dst + G::kOffVd, ph + PG::kOffVd + t0 * PG::kVdRow, kStageKeys * PG::kVdRow, bar);
+                    }
+                    if constexpr (PG::kVhRow > 0)
+                        bulk_load(dst + G::kOffVh, ph + PG::kOffVh + t0 * PG::kVhRow, kStageKeys * PG::kVhRow, bar);
+                    if constexpr (PG::kVmRow > 0)
+                        bulk_load(dst + G::kOffVm, ph + PG::kOffVm + t0 * PG::kVmRow, kStageKeys * PG::kVmRow, bar);
+                }
+                __syncwarp();
+                ++issued;
+            }
+            cur = stop;
+            ++n_pieces;
+        }
+        // a wait gave up: the copies in flight land before the memory is given back
+        for (int k = max(0, issued - kStages); !ok && k < issued; ++k)
+            mbar_wait_bounded(&full[k % kStages], (k / kStages) & 1, a.batch.status);
+        return;
+    }
+
+    // ============================ consumers ============================
+    const int g = lane >> 2, q = lane & 3;
+    const bool formed = a.softcap > 0.0f || a.slopes;  // scores need more than a scale
+    int used = 0;                                      // stages so far
+    // a barrier of the four consumer warps whose wait is bounded like every other
+    // here: a warp whose wait gave up leaves nobody behind for good
+    uint32_t c_phase = 0;
+    auto consumers_sync = [&]() -> bool {
+        __syncwarp();
+        if (lane == 0) arrive(c_bar);
+        const bool ok = mbar_wait_bounded(c_bar, c_phase, a.batch.status, kWaitNs);
+        c_phase ^= 1;
+        return __all_sync(0xffffffffu, ok);
+    };
+    for (int n = 0;; ++n) {
+        Piece<ROWS>& p = pieces[n & 1];
+        if (!mbar_wait_bounded(&p_full[n & 1], (n >> 1) & 1, a.batch.status, kWaitNs)) return;
+        if (p.n_stages < 0) return;
+        float o[8][NT][4];
+        float ref[NT][2], l[NT][2], sc[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[t][nt][j] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                ref[nt][j] = -CUDART_INF_F;
+                l[nt][j] = 0.0f;
+                sc[nt][j] = p.scale[8 * nt + 2 * q + j];
+            }
+        }
+        const uint8_t* sq = p.q + g * kQRow + 8 * q;  // this lane's operand: row g, dims 16 c + 4 q ..
+        bool ok = true;
+        for (int i = 0; i < p.n_stages; ++i, ++used) {
+            const int buf = used % kStages;
+            ok = mbar_wait_bounded(&full[buf], (used / kStages) & 1, a.batch.status, kWaitNs);
+            if (!__all_sync(0xffffffffu, ok)) return;
+            const uint8_t* sb = smem + buf * G::kBytes;
+            const int key0 = (p.first_stage + i) * kStageKeys;  // the stage's first key
+            const int wk = warp * 32;                           // this warp's first key in it
+
+            // ---- S^T = K Q^T: two tiles of 16 keys ----
+            float s[2][NT][4];
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[mt][nt][j] = 0.0f;
+            // ldmatrix rows of this lane: matrices 0, 1 = keys 0..7, 8..15 of a
+            // chunk, 2, 3 = the next chunk
+            const int lk = wk + (lane & 7) + ((lane >> 3) & 1) * 8, lc = lane >> 4;
+            if constexpr (KT == kKF16) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {  // 16 dims: two 8-dim chunks
+                    uint2 qb[NT];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        // operand pairs (dims 16c + 2q, +1) and (16c + 8 + 2q, +1)
+                        const uint8_t* r = p.q + (8 * nt + g) * kQRow + 32 * c + 4 * q;
+                        qb[nt].x = *reinterpret_cast<const uint32_t*>(r);
+                        qb[nt].y = *reinterpret_cast<const uint32_t*>(r + 16);
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt) {
+                        const int key = lk + 16 * mt, ch = (2 * c & 7) + lc;
+                        uint32_t w[4];
+                        ldsm4(smem_u32(sb + (c >> 2) * kStageKeys * 128 + key * 128 + ((ch ^ (key & 7)) << 4)), w);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma(s[mt][nt], w, qb[nt].x, qb[nt].y);
+                    }
+                }
+            } else {
+                uint2 kd[2][2];  // the four block scales of keys g, g + 8 of each tile
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        kd[mt][j] = *reinterpret_cast<const uint2*>(sb + G::kOffKd + (wk + 16 * mt + 8 * j + g) * 8);
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) {
+                    uint2 qb[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            qb[nt][c] = *reinterpret_cast<const uint2*>(sq + 8 * nt * kQRow + 32 * (2 * b + c));
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt) {
+                        const int key = lk + 16 * mt, ch = 2 * b + lc;
+                        uint32_t w[4], k0[4], k1[4];
+                        ldsm4(smem_u32(sb + key * 128 + ((ch ^ (key & 7)) << 4)), w);
+                        s8x4(w[0], 0x4140, 0x4342, k0[0], k0[2]);
+                        s8x4(w[1], 0x4140, 0x4342, k0[1], k0[3]);
+                        s8x4(w[2], 0x4140, 0x4342, k1[0], k1[2]);
+                        s8x4(w[3], 0x4140, 0x4342, k1[1], k1[3]);
+                        const __half2 d0 = u2h(b < 2 ? kd[mt][0].x : kd[mt][0].y), d1 = u2h(b < 2 ? kd[mt][1].x : kd[mt][1].y);
+                        const float f0 = (b & 1) ? __high2float(d0) : __low2float(d0);
+                        const float f1 = (b & 1) ? __high2float(d1) : __low2float(d1);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                            mma(c, k0, qb[nt][0].x, qb[nt][0].y);
+                            mma(c, k1, qb[nt][1].x, qb[nt][1].y);
+                            s[mt][nt][0] = fmaf(f0, c[0], s[mt][nt][0]);
+                            s[mt][nt][1] = fmaf(f0, c[1], s[mt][nt][1]);
+                            s[mt][nt][2] = fmaf(f1, c[2], s[mt][nt][2]);
+                            s[mt][nt][3] = fmaf(f1, c[3], s[mt][nt][3]);
+                        }
+                    }
+                }
+            }
+
+            // ---- scores in the log2 domain; element j: key g + 8 (j / 2), row 2 q + (j & 1) ----
+            const bool all_seen = key0 >= p.full_from && key0 + kStageKeys <= p.full_to;
+            bool above = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[mt][nt][j] *= sc[nt][j & 1];
+                if (formed) {
+#pragma unroll
+                    for (int jr = 0; jr < 2; ++jr) {
+                        const int r = 8 * nt + 2 * q + jr;
+                        const float slope = p.slope[r];
+                        const int pos = p.pos[r];
+#pragma unroll
+                        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                            for (int jk = 0; jk < 2; ++jk)
+                                s[mt][nt][2 * jk + jr] =
+                                    score_log2(a, s[mt][nt][2 * jk + jr], slope, pos, key0 + wk + 16 * mt + 8 * jk + g);
+                    }
+                }
+                if (!all_seen) {
+#pragma unroll
+                    for (int jr = 0; jr < 2; ++jr) {
+                        const int first = p.first[8 * nt + 2 * q + jr], end = p.end[8 * nt + 2 * q + jr];
+#pragma unroll
+                        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                            for (int jk = 0; jk < 2; ++jk) {
+                                const int key = key0 + wk + 16 * mt + 8 * jk + g;
+                                if (key < first || key >= end) s[mt][nt][2 * jk + jr] = -CUDART_INF_F;
+                            }
+                    }
+                }
+#pragma unroll
+                for (int jr = 0; jr < 2; ++jr) {
+                    const float top = fmaxf(fmaxf(s[0][nt][jr], s[0][nt][2 + jr]), fmaxf(s[1][nt][jr], s[1][nt][2 + jr]));
+                    above |= top > ref[nt][jr] + 9.0f;
+                }
+            }
+            // The reference of a row is 6 below a maximum seen so far, and moves only
+            // when a score passes it by 9: weights stay within 2^9, most near 2^6.
+            if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int jr = 0; jr < 2; ++jr) {
+                        float top = fmaxf(fmaxf(s[0][nt][jr], s[0][nt][2 + jr]), fmaxf(s[1][nt][jr], s[1][nt][2 + jr]));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)) - 6.0f;
+                        const float now = fmaxf(ref[nt][jr], top);
+                        const float f = now == ref[nt][jr] ? 1.0f : exp2_fast(ref[nt][jr] - now);
+                        ref[nt][jr] = now;
+                        l[nt][jr] *= f;
+#pragma unroll
+                        for (int t = 0; t < 8; ++t) {
+                            o[t][nt][jr] *= f;
+                            o[t][nt][2 + jr] *= f;
+                        }
+                    }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int jr = 0; jr < 2; ++jr) {
+                    const float r = ref[nt][jr] == -CUDART_INF_F ? 0.0f : ref[nt][jr];
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                        for (int jk = 0; jk < 2; ++jk) {
+                            const float w = exp2_fast(s[mt][nt][2 * jk + jr] - r);
+                            s[mt][nt][2 * jk + jr] = w;
+                            l[nt][jr] += w;
+                        }
+                }
+
+            // ---- O^T += V^T P^T, 16 keys at a time ----
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+                // weights with keys along the pair: [nt][keys 2q,2q+1 | 8+2q, 8+2q+1], and
+                // what their rounding to fp16 left
+                uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int jk = 0; jk < 2; ++jk) {
+                        const float x = s[mt][nt][2 * jk], y = s[mt][nt][2 * jk + 1];
+                        const __half2 hi = __floats2half2_rn(x, y);
+                        ph[nt][jk] = movm(h2u(hi));
+                        if (a.precise) {
+                            const float2 f = __half22float2(hi);
+                            pl[nt][jk] = movm(h2u(__floats2half2_rn(x - f.x, y - f.y)));
+                        }
+                    }
+                // keys that do not exist hold anything: their scales (or values) become 0
+                uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+                if (!all_seen) {
+#pragma unroll
+                    for (int jk = 0; jk < 2; ++jk) {
+                        const int key = key0 + wk + 16 * mt + 8 * jk + 2 * q;
+                        keep[jk] = (key < p.n_keys ? 0xffffu : 0u) | (key + 1 < p.n_keys ? 0xffff0000u : 0u);
+                    }
+                }
+                uint4 dv[2], mv[2];  // four block scales (minima) of keys 2q and 2q + 1 of each half
+                if constexpr (VT != kVF16) {
+#pragma unroll
+                    for (int jk = 0; jk < 2; ++jk) {
+                        dv[jk] = *reinterpret_cast<const uint4*>(sb + G::kOffVd + (wk + 16 * mt + 8 * jk + 2 * q) * 8);
+                        if constexpr (v_has_min(VT))
+                            mv[jk] = *reinterpret_cast<const uint4*>(sb + G::kOffVm + (wk + 16 * mt + 8 * jk + 2 * q) * 8);
+                    }
+                }
+                // block b of a key pair: (key 2q, key 2q + 1)
+                auto pair = [&](const uint4& v, int b) -> uint32_t {
+                    return (b < 2) ? __byte_perm(v.x, v.z, (b & 1) ? 0x7632 : 0x5410)
+                                   : __byte_perm(v.y, v.w, (b & 1) ? 0x7632 : 0x5410);
+                };
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) {
+                    uint32_t bh[NT][2], bl[NT][2];
+                    __half2 dvp[2], mvp[2];
+                    if constexpr (VT != kVF16) {
+#pragma unroll
+                        for (int jk = 0; jk < 2; ++jk) {
+                            dvp[jk] = u2h(pair(dv[jk], b) & keep[jk]);
+                            if constexpr (v_has_min(VT)) mvp[jk] = u2h(pair(mv[jk], b) & keep[jk]);
+                        }
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int jk = 0; jk < 2; ++jk) {
+                            if constexpr (v_a_is_p(VT)) {
+                                bh[nt][jk] = ph[nt][jk];
+                                bl[nt][jk] = pl[nt][jk];
+                            } else {
+                                const __half2 hi = __hmul2(u2h(ph[nt][jk]), dvp[jk]);
+                                bh[nt][jk] = h2u(hi);
+                                if (a.precise)  // the product's own error (exact by fma) and the low term
+                                    bl[nt][jk] = h2u(__hfma2(u2h(pl[nt][jk]), dvp[jk], __hfma2(u2h(ph[nt][jk]), dvp[jk], __hneg2(hi))));
+                            }
+                        }
+                    // the block's two tiles of 16 dims: rows g, g + 8 of tile e
+                    uint32_t va[2][4];
+                    if constexpr (VT == kVF16) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int ch = 2 * (2 * b + e);  // 8-dim chunk; matrices: keys 0..7, 8..15 of it, then of the next
+                            const int key = wk + 16 * mt + (lane & 7) + ((lane >> 3) & 1) * 8, cl = (ch & 7) + (lane >> 4);
+                            uint32_t w[4];
+                            ldsm4t(smem_u32(sb + G::kOffV + (ch >> 3) * kStageKeys * 128 + key * 128 + ((cl ^ (key & 7)) << 4)), w);
+                            va[e][0] = w[0] & keep[0];
+                            va[e][1] = w[2] & keep[0];
+                            va[e][2] = w[1] & keep[1];
+                            va[e][3] = w[3] & keep[1];
+                        }
+                    } else if constexpr (VT == kVQ8_0) {
+                        const int key = wk + 16 * mt + (lane & 7) + ((lane >> 3) & 1) * 8, ch = 2 * b + (lane >> 4);
+                        uint32_t w[4];
+                        ldsm4t(smem_u32(sb + G::kOffV + key * 128 + ((ch ^ (key & 7)) << 4)), w);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {  // word: (key 2q: dims 2g, 2g+1 | key 2q+1: the same)
+                            s8x4(w[2 * e], 0x4240, 0x4341, va[e][0], va[e][1]);
+                            s8x4(w[2 * e + 1], 0x4240, 0x4341, va[e][2], va[e][3]);
+                        }
+                    } else {
+                        uint32_t w[2];
+                        const int key = wk + 16 * mt + (lane & 7) + ((lane >> 3) & 1) * 8, ch = b;
+                        asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];"
+                                     : "=r"(w[0]), "=r"(w[1])
+                                     : "r"(smem_u32(sb + G::kOffV + key * 64 + ((ch ^ ((key >> 1) & 3)) << 4))) : "memory");
+#pragma unroll
+                        for (int jk = 0; jk < 2; ++jk) {
+                            // word: (key 2q: bytes 2g, 2g+1 | key 2q+1: the same); a byte's low nibble is
+                            // dim 2g (+1), its high nibble dim 16 + 2g (+1)
+                            uint32_t f[2][2] = {{0u, 0u}, {0u, 0u}};  // fifth bits in place, [nibble][byte]
+                            if constexpr (v_has_fifth(VT)) {
+                                const uint8_t* hp = sb + G::kOffVh + (wk + 16 * mt + 8 * jk + 2 * q) * 16 + 4 * b;
+                                const uint32_t h0 = *reinterpret_cast<const uint32_t*>(hp) >> (2 * g);
+                                const uint32_t h1 = *reinterpret_cast<const uint32_t*>(hp + 16) >> (2 * g);
+                                const uint32_t u = __byte_perm(h0, h1, 0x5410), v = __byte_perm(h0, h1, 0x7632);
+                                f[0][0] = (u << 4) & 0x00100010u;
+                                f[0][1] = (u << 3) & 0x00100010u;
+                                f[1][0] = (v << 8) & 0x01000100u;
+                                f[1][1] = (v << 7) & 0x01000100u;
+                            }
+                            constexpr float kZero = v_has_min(VT) ? 0.0f : (VT == kVQ5_0 ? 16.0f : 8.0f);
+                            const __half2 z0 = __float2half2_rn(1024.0f + kZero), z1 = __float2half2_rn(-64.0f - kZero);
+                            const __half2 six = __float2half2_rn(0.0625f);
+                            const uint32_t y = w[jk] >> 8;
+                            __half2 c[2][2];
+                            c[0][0] = __hsub2(u2h((w[jk] & 0x000f000fu) | 0x64006400u | f[0][0]), z0);
+                            c[0][1] = __hsub2(u2h((y & 0x000f000fu) | 0x64006400u | f[0][1]), z0);
+                            c[1][0] = __hfma2(u2h((w[jk] & 0x00f000f0u) | 0x64006400u | f[1][0]), six, z1);
+                            c[1][1] = __hfma2(u2h((y & 0x00f000f0u) | 0x64006400u | f[1][1]), six, z1);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                                for (int u = 0; u < 2; ++u) {
+                                    if constexpr (v_has_min(VT)) c[e][u] = __hfma2(c[e][u], dvp[jk], mvp[jk]);
+                                    va[e][2 * jk + u] = h2u(c[e][u]);
+                                }
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma(o[2 * b + e][nt], va[e], bh[nt][0], bh[nt][1]);
+                            if (a.precise) mma(o[2 * b + e][nt], va[e], bl[nt][0], bl[nt][1]);
+                        }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) arrive(&empty[buf]);
+        }
+
+        // ---- the piece's end: join the warps, 8 rows at a time ----
+        const bool bad = p.bad;
+        if (bad && tid == 0 && a.batch.status) atomicOr(a.batch.status, kErrBadPage);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            if (8 * nt >= p.rows) break;  // uniform
+#pragma unroll
+            for (int jr = 0; jr < 2; ++jr) {
+                float sum = l[nt][jr];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                if (g == 0) {
+                    sml[(warp * 8 + 2 * q + jr) * 2] = ref[nt][jr];
+                    sml[(warp * 8 + 2 * q + jr) * 2 + 1] = bad ? CUDART_NAN_F : sum;
+                }
+                float* dst = red + (warp * 8 + 2 * q + jr) * kRedRow;
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    if constexpr (VT == kVF16) {  // tile t: dims 16 t + g and 16 t + 8 + g
+                        dst[16 * t + g] = o[t][nt][jr];
+                        dst[16 * t + 8 + g] = o[t][nt][2 + jr];
+                    } else {  // dims 16 t + 2 g, + 1
+                        *reinterpret_cast<float2*>(dst + 16 * t + 2 * g) = make_float2(o[t][nt][jr], o[t][nt][2 + jr]);
+                    }
+                }
+            }
+            if (!consumers_sync()) return;
+#pragma unroll
+            for (int rr = 0; rr < 2; ++rr) {
+                const int r = warp + kConsumers * rr, pr = 8 * nt + r;
+                if (pr >= p.rows || p.token[pr] < 0) continue;
+                float M = -CUDART_INF_F, L = 0.0f;
+                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int w = 0; w < kConsumers; ++w)
+                    join(acc, M, L, *reinterpret_cast<const float4*>(red + (w * 8 + r) * kRedRow + 4 * lane), sml[(w * 8 + r) * 2],
+                         sml[(w * 8 + r) * 2 + 1]);
+                if (p.slot < 0) {
+                    finish_row<VT, KT>(a, p.seq, p.token[pr], p.head[pr], acc, M, L);
+                } else {
+                    float* rec = a.records + ((size_t)(blockIdx.x * 2 + p.slot) * kFewRowsMax + pr) * kRecordFloats;
+                    *reinterpret_cast<float4*>(rec + 4 * lane) = acc;
+                    if (lane == 0) *reinterpret_cast<float2*>(rec + 128) = make_float2(M, L);
+                }
+            }
+            if (!consumers_sync()) return;
+        }
+        if (p.slot >= 0) {
+            // ---- a shared unit: the last CTA to arrive joins the records ----
+            __threadfence();
+            if (!consumers_sync()) return;
+            if (tid == 0) {
+                const int before = atomicAdd(&a.counters[p.cta0], 1);
+                const bool last = before == p.n_ctas - 1;
+                if (last) a.counters[p.cta0] = 0;  // ready for the next call
+                *sLast = last;
+            }
+            if (!consumers_sync()) return;
+            if (*sLast) {
+                __threadfence();
+                for (int pr = warp; pr < p.rows; pr += kConsumers) {
+                    if (p.token[pr] < 0) continue;
+                    // the first CTA began the unit, the others continue it
+                    auto record = [&](int c) {
+                        return a.records + ((size_t)((p.cta0 + c) * 2 + (c == 0 ? 1 : 0)) * kFewRowsMax + pr) * kRecordFloats;
+                    };
+                    float M = -CUDART_INF_F, L = 0.0f;
+                    for (int c = lane; c < p.n_ctas; c += 32) M = fmaxf(M, __ldcg(record(c) + 128));
+#pragma unroll
+                    for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+                    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+                    for (int c = 0; c < p.n_ctas; ++c) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(record(c)) + lane);
+                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(record(c) + 128));
+                        const float w = ml.x == M ? 1.0f : exp2_fast(ml.x - M);
+                        acc.x = fmaf(v.x, w, acc.x);
+                        acc.y = fmaf(v.y, w, acc.y);
+                        acc.z = fmaf(v.z, w, acc.z);
+                        acc.w = fmaf(v.w, w, acc.w);
+                        L = fmaf(ml.y, w, L);
+                    }
+                    finish_row<VT, KT>(a, p.seq, p.token[pr], p.head[pr], acc, M, L);
+                }
+            }
+        }
+        if (!consumers_sync()) return;  // sLast and the join buffer are free again
+        if (lane == 0) arrive(&p_empty[n & 1]);
+    }
+}
+
+template <int VT, int KT, int NT>
+cudaError_t launch(const AttendPagesArgs& a, const PageMaps& maps, int n_sms, cudaStream_t s) {
+    using G = Geo<VT, KT, NT>;
+    // the shared-memory opt-in is per device
+    static std::atomic<unsigned long long> configured{0};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 64 || !(configured.load(std::memory_order_acquire) & (1ull << dev))) {
+        const cudaError_t e = cudaFuncSetAttribute(attend_few_kernel<VT, KT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) configured.fetch_or(1ull << dev, std::memory_order_acq_rel);
+    }
+    attend_few_kernel<VT, KT, NT><<<std::min(kFewCtas, n_sms * G::kPerSm), kThreads, G::kSmem, s>>>(a, maps);
+    return cudaGetLastError();
+}
+
+template <int VT, int KT>
+cudaError_t by_rows(const AttendPagesArgs& a, const PageMaps& maps, int unit_rows, int n_sms, cudaStream_t s) {
+    switch (unit_rows) {
+        case 8: return launch<VT, KT, 1>(a, maps, n_sms, s);
+        case 16: return launch<VT, KT, 2>(a, maps, n_sms, s);
+        default: return launch<VT, KT, 4>(a, maps, n_sms, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_attend_few(const AttendPagesArgs& a, const PageMaps& maps, int unit_rows, int n_sms, cudaStream_t s) {
+    if (a.pool.k_type == kKF16) return by_rows<kVF16, kKF16>(a, maps, unit_rows, n_sms, s);
+    switch (a.pool.v_type) {
+        case kVF16: return by_rows<kVF16, kKQ8_0>(a, maps, unit_rows, n_sms, s);
+        case kVQ4_1: return by_rows<kVQ4_1, kKQ8_0>(a, maps, unit_rows, n_sms, s);
+        case kVQ5_0: return by_rows<kVQ5_0, kKQ8_0>(a, maps, unit_rows, n_sms, s);
+        case kVQ5_1: return by_rows<kVQ5_1, kKQ8_0>(a, maps, unit_rows, n_sms, s);
+        case kVQ8_0: return by_rows<kVQ8_0, kKQ8_0>(a, maps, unit_rows, n_sms, s);
+        default: return by_rows<kVQ4_0, kKQ8_0>(a, maps, unit_rows, n_sms, s);
+    }
+}
+
+}  // namespace kvs

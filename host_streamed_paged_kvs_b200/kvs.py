@@ -35,6 +35,9 @@ KVS_FLAG_PROFILE = 1
 KVS_FLAG_PHASE_ARENA = 2
 KVS_PHASE_PREFILL = 0
 KVS_PHASE_DECODE = 1
+KVS_DT_F16 = 0
+KVS_DT_BF16 = 1
+KVS_DT_F32 = 2
 
 ERROR_NAMES = {0: "KVS_OK", -1: "KVS_E_INVAL", -2: "KVS_E_ARENA", -3: "KVS_E_WIDTH",
                -4: "KVS_E_ORDER", -5: "KVS_E_CUDA", -6: "KVS_E_TIMEOUT", -7: "KVS_E_NOMEM"}
@@ -47,7 +50,7 @@ EXPORTS = ["kvs_resolve_config", "kvs_page_bytes", "kvs_plan_page", "kvs_plan_ri
            "kvs_measure_h2d", "kvs_attend_pages_static", "kvs_selftest_bounded_wait",
            "kvs_last_error", "kvs_eject_init", "kvs_eject_step", "kvs_draft_capacity_pages",
            "kvs_phase_layout", "kvs_set_phase", "kvs_pin", "kvs_draft_eject", "kvs_draft_restore",
-           "kvs_get_arena"]
+           "kvs_get_arena", "kvs_append_pages", "kvs_read_pages", "kvs_attend_pages", "kvs_attend_pages_workspace"]
 
 
 class kvs_config(ctypes.Structure):
@@ -101,6 +104,35 @@ class kvs_eject_state(ctypes.Structure):
     _fields_ = [("draft_active", ctypes.c_int), ("streak", ctypes.c_int)]
 
 
+class kvs_page_pool(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
+                ("type_k", ctypes.c_int), ("type_v", ctypes.c_int)]
+
+
+class kvs_page_batch(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int), ("n_rows", ctypes.c_int), ("max_new", ctypes.c_int),
+                ("q_start", ctypes.c_void_p), ("seq_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int), ("status", ctypes.c_void_p)]
+
+
+class kvs_page_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong)]
+
+
+class kvs_rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("positions", ctypes.c_void_p), ("pos_offset", ctypes.c_int), ("mscale", ctypes.c_float)]
+
+
+class kvs_score(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int),
+                ("alibi_slopes", ctypes.c_void_p), ("first_key", ctypes.c_void_p), ("end_key", ctypes.c_void_p)]
+
+
+class kvs_page_prefix(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("n_tokens", ctypes.c_int)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -141,6 +173,13 @@ def _load():
     L.kvs_draft_eject.argtypes = [vp, vp]
     L.kvs_draft_restore.argtypes = [vp, vp]
     L.kvs_get_arena.argtypes = [vp, cp(kvs_arena_status)]
+    pool, batch, rows = cp(kvs_page_pool), cp(kvs_page_batch), cp(kvs_page_rows)
+    L.kvs_append_pages.argtypes = [pool, batch, i, rows, rows, i, rows, rows, cp(kvs_rope), vp]
+    L.kvs_read_pages.argtypes = [pool, batch, i, rows, rows, vp]
+    L.kvs_attend_pages.argtypes = [pool, batch, i, i, rows, i, rows, vp, cp(kvs_score), cp(kvs_page_prefix), vp,
+                                   ctypes.c_size_t, vp]
+    L.kvs_attend_pages_workspace.argtypes = [batch, i, i]
+    L.kvs_attend_pages_workspace.restype = ctypes.c_size_t
     return L
 
 
@@ -326,6 +365,156 @@ def kvs_attend_pages_static(pages, n_pages, n_tokens, n_q_heads, n_kv_heads, pos
 
 
 KVS_ERR_WAIT_TIMEOUT = 1
+KVS_ERR_BAD_PAGE = 2
+
+
+# ---- batches over caller-owned pages (include/kvs.h) ----------------------
+# The make_* functions describe buffers once; the descriptors keep the tensors
+# alive and can be used for any number of calls, captured ones too.
+
+_DTYPES = {"torch.float16": KVS_DT_F16, "torch.bfloat16": KVS_DT_BF16, "torch.float32": KVS_DT_F32}
+
+
+def _bad(msg: str):
+    raise KvsError(KVS_E_INVAL, msg)
+
+
+def _int32(x, what: str, least: int = 0) -> Optional[int]:
+    """Address of a contiguous int32 device tensor of at least `least` values (None -> NULL)."""
+    if x is None:
+        return None
+    if str(x.dtype) != "torch.int32" or not x.is_contiguous() or x.numel() < least or not x.is_cuda:
+        _bad(f"{what}: a contiguous int32 device tensor of at least {least} values is wanted")
+    return x.data_ptr()
+
+
+def _float32(x, what: str, least: int) -> Optional[int]:
+    if x is None:
+        return None
+    if str(x.dtype) != "torch.float32" or not x.is_contiguous() or x.numel() < least or not x.is_cuda:
+        _bad(f"{what}: a contiguous float32 device tensor of at least {least} values is wanted")
+    return x.data_ptr()
+
+
+def make_page_pool(pages, n_kv_heads: int, type_k: int = KVS_TYPE_Q8_0, type_v: int = KVS_TYPE_Q4_0) -> kvs_page_pool:
+    """A pool of pages: a contiguous uint8 device tensor of whole pages."""
+    head = kvs_page_bytes(make_config(1, n_kv_heads, n_kv_heads, 256, 1, type_k=type_k, type_v=type_v))
+    if not head:
+        _bad("unsupported K/V type pair or heads")
+    if not pages.is_contiguous() or not pages.is_cuda or pages.element_size() != 1 or pages.numel() % head or not pages.numel():
+        _bad(f"pages: a contiguous uint8 device tensor of whole pages of {head} bytes is wanted")
+    p = kvs_page_pool(pages.data_ptr(), pages.numel() // head, n_kv_heads, type_k, type_v)
+    p.keep = pages
+    return p
+
+
+def make_page_batch(q_start, seq_len, page_table, n_rows: int, max_new: int = 0, status=None) -> kvs_page_batch:
+    """q_start int32 [n_seqs + 1], seq_len int32 [n_seqs], page_table int32 [n_seqs, entries], all on the device."""
+    n = seq_len.numel()
+    if page_table.dim() != 2 or page_table.shape[0] != n:
+        _bad("page_table: [n_seqs, entries] is wanted")
+    b = kvs_page_batch(n, n_rows, max_new, _int32(q_start, "q_start", n + 1), _int32(seq_len, "seq_len"),
+                       _int32(page_table, "page_table"), page_table.shape[1], _int32(status, "status", 1))
+    b.keep = (q_start, seq_len, page_table, status)
+    return b
+
+
+def make_rope(inv_freq, rot_dim: int = 128, interleaved: bool = False, positions=None, pos_offset: int = 0,
+              mscale: float = 1.0) -> kvs_rope:
+    """inv_freq float32 [rot_dim / 2]; positions int32 [n_rows] or None (own position + pos_offset)."""
+    r = kvs_rope(_float32(inv_freq, "inv_freq", rot_dim // 2), rot_dim, int(interleaved), _int32(positions, "positions"),
+                 pos_offset, mscale)
+    r.keep = (inv_freq, positions)
+    return r
+
+
+def make_score(scale: float = 0.0, softcap: float = 0.0, window: int = 0, alibi_slopes=None, first_key=None,
+               end_key=None) -> kvs_score:
+    """alibi_slopes float32 [n_q_heads]; first_key, end_key int32 [n_rows]."""
+    s = kvs_score(scale, softcap, window, _float32(alibi_slopes, "alibi_slopes", 1), _int32(first_key, "first_key"),
+                  _int32(end_key, "end_key"))
+    s.keep = (alibi_slopes, first_key, end_key)
+    return s
+
+
+def make_page_prefix(page_table, n_tokens: int) -> kvs_page_prefix:
+    """page_table int32 [pages of n_tokens]."""
+    p = kvs_page_prefix(_int32(page_table, "prefix page_table", -(-n_tokens // 256)), n_tokens)
+    p.keep = page_table
+    return p
+
+
+def _rows(x, batch, heads: int, what: str):
+    """(descriptor, dtype code) of a [rows, heads, 128] device tensor, strides as they are."""
+    dt = _DTYPES.get(str(x.dtype))
+    shape = x.shape
+    if dt is None or len(shape) != 3 or shape[0] < batch.n_rows or shape[1] != heads or shape[2] != 128 or \
+            (x.stride(2) != 1) or not x.is_cuda:
+        _bad(f"{what}: a float16, bfloat16 or float32 device tensor [rows >= {batch.n_rows}, {heads}, 128] with "
+             "contiguous heads is wanted")
+    return kvs_page_rows(x.data_ptr(), x.stride(0), x.stride(1)), dt
+
+
+def _same(a: int, b: int, what: str) -> int:
+    if a != b:
+        _bad(f"{what} must have the same dtype")
+    return a
+
+
+def kvs_append_pages(pool, batch, k, v, q=None, q_out=None, rope=None, stream=None) -> None:
+    """Rotate K (and Q into q_out), quantize K and V and write them to the batch's pages."""
+    kr, dt = _rows(k, batch, pool.n_kv_heads, "k")
+    vr, dv = _rows(v, batch, pool.n_kv_heads, "v")
+    _same(dt, dv, "k and v")
+    qr = qo = None
+    heads = 0
+    if q is not None or q_out is not None:
+        if q is None or q_out is None or q.dim() != 3:
+            _bad("q and q_out go together, [rows, heads, 128]")
+        heads = q.shape[1]
+        (qr, d0), (qo, d1) = _rows(q, batch, heads, "q"), _rows(q_out, batch, heads, "q_out")
+        _same(_same(dt, d0, "k and q"), d1, "k and q_out")
+    if rope is not None and rope.keep[1] is not None and rope.keep[1].numel() < batch.n_rows:
+        _bad("positions: one per row is wanted")
+    _check(lib.kvs_append_pages(pool, batch, dt, kr, vr, heads, qr, qo, rope, _stream(stream)))
+
+
+def kvs_read_pages(pool, batch, k=None, v=None, stream=None) -> None:
+    """Write the values of the batch's rows, read from its pages, to k and / or v."""
+    kr, dk = _rows(k, batch, pool.n_kv_heads, "k") if k is not None else (None, None)
+    vr, dv = _rows(v, batch, pool.n_kv_heads, "v") if v is not None else (None, None)
+    if dk is None and dv is None:
+        _bad("neither k nor v is wanted")
+    dt = _same(dk, dv, "k and v") if dk is not None and dv is not None else (dk if dv is None else dv)
+    _check(lib.kvs_read_pages(pool, batch, dt, kr, vr, _stream(stream)))
+
+
+def kvs_attend_pages_workspace(batch, n_q_heads: int, n_kv_heads: int) -> int:
+    """Bytes of workspace (a zero-filled device buffer) for calls up to this batch's size."""
+    n = lib.kvs_attend_pages_workspace(batch, n_q_heads, n_kv_heads)
+    if not n:
+        _bad(kvs_last_error())
+    return n
+
+
+def kvs_attend_pages(pool, batch, q, out, lse=None, score=None, prefix=None, workspace=None, stream=None) -> None:
+    """Attention of the batch's rows over their pages (after a shared prefix); see include/kvs.h."""
+    if q.dim() != 3:
+        _bad("q: [rows, heads, 128] is wanted")
+    heads = q.shape[1]
+    (qr, dq), (orow, do) = _rows(q, batch, heads, "q"), _rows(out, batch, heads, "out")
+    if workspace is None:
+        _bad("a workspace is wanted (kvs_attend_pages_workspace bytes, zero-filled)")
+    if lse is not None and (str(lse.dtype) != "torch.float32" or not lse.is_contiguous() or lse.numel() < batch.n_rows * heads):
+        _bad("lse: a contiguous float32 tensor [n_rows, heads] is wanted")
+    if score is not None:
+        slopes, first, end = score.keep
+        if (slopes is not None and slopes.numel() < heads) or any(x is not None and x.numel() < batch.n_rows
+                                                                  for x in (first, end)):
+            _bad("score: alibi_slopes has one value a head, first_key and end_key one a row")
+    _check(lib.kvs_attend_pages(pool, batch, dq, heads, qr, do, orow, _addr(lse), score, prefix, workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(), _stream(stream)))
+
 
 
 def kvs_selftest_bounded_wait(device: int = 0, limit_s: float = 0.2) -> int:

@@ -415,12 +415,162 @@ int kvs_attend_pages_static(const void* pages, int n_pages, int n_tokens, int n_
                             int n_kv_heads, int pos0, int n_q, const void* q_f16, float* out,
                             float* lse, void* stream);
 
+/* ---- batches over caller-owned pages -----------------------------------------
+ * Append, read-back and attention for a batch of sequences whose quantized
+ * pages live in one caller-owned device pool and are found through page
+ * tables: what a serving engine with its own page allocator needs beside the
+ * handle calls above (whose pool streams from host memory).  No handle, no
+ * allocation; every call is one to three kernels on `stream`, can be captured
+ * into a CUDA graph, and reads the batch (row ranges, lengths, page tables)
+ * from device memory when it runs, so a captured graph can be replayed after
+ * those arrays, or the tensors' contents, have changed.
+ *
+ * The calls check what the host can see and return KVS_E_INVAL: null or
+ * misaligned pointers, negative sizes, unsupported types, strides that the
+ * vector accesses cannot take.  What only the device can see is bounded
+ * there: rows beyond n_rows, lengths beyond the page table and page numbers
+ * outside the pool are never followed.  A bad page number gives NaN in the
+ * rows of a sequence (of the batch, for the prefix) that would have read the
+ * page, is not written by an append, and sets KVS_ERR_BAD_PAGE in *status.
+ *
+ * All device pointers of a call belong to one device, the one that owns
+ * pool->pages; it need not be the current one.  `stream` must be a stream of
+ * that device. */
+#define KVS_DT_F16  0
+#define KVS_DT_BF16 1
+#define KVS_DT_F32  2
+
+/* A pool of pages.  A page is 256 tokens of all kv heads, [n_kv_heads][page
+ * head], in the layout that kvs_config.type_k / type_v describe (and that
+ * kvs_append writes): for K Q8_0 / V Q4_0 the page head is Kq int8 [256][128]
+ * | Kd fp16 [256][4] | Vq u8 [256][4][16] | Vd fp16 [256][4].  Field order:
+ * K codes, K scales, V codes, V fifth bits, V scales, V minima. */
+typedef struct kvs_page_pool {
+    void* pages;     /* device, 16-byte aligned */
+    int n_pages;
+    int n_kv_heads;
+    int type_k, type_v; /* the pairs kvs_config takes */
+} kvs_page_pool;
+
+/* The batch: sequence i has the rows q_start[i] .. q_start[i+1]-1 of the K, V,
+ * Q and output tensors as its new tokens, which sit at the end of its
+ * seq_len[i] cached tokens (new token t of n at own position seq_len[i] - n +
+ * t), and its tokens 256 j .. 256 j + 255 in page page_table[i][j].  Rows
+ * outside every sequence's range (padding) are neither read nor written.
+ * q_start does not decrease.  Sequences may have no rows and no tokens.  More
+ * rows than tokens is allowed: rows at negative positions append nothing, and
+ * see nothing of their own pages. */
+typedef struct kvs_page_batch {
+    int n_seqs;            /* >= 0 */
+    int n_rows;            /* rows of the tensors; a bound on q_start[n_seqs] */
+    int max_new;           /* rows of the longest sequence, if known (0 = not known): kernels are
+                              chosen by it; a sequence with more rows is right, only slower */
+    const int* q_start;    /* device [n_seqs + 1] */
+    const int* seq_len;    /* device [n_seqs], tokens after the append */
+    const int* page_table; /* device [n_seqs][table_stride] */
+    int table_stride;      /* page table entries per sequence; those past a sequence's
+                              last page may hold anything */
+    int* status;           /* device word that KVS_ERR_* bits are or-ed into, or NULL */
+} kvs_page_batch;
+
+/* A [n_rows][heads][128] tensor of KVS_DT_* values with its strides, in
+ * values; the 128 values of a head are contiguous.  Address and strides must
+ * be multiples of 16 bytes. */
+typedef struct kvs_page_rows {
+    void* data;
+    long long row_stride, head_stride;
+} kvs_page_rows;
+
+/* Rotary position embedding of K (and Q) rows: the pair (x0, x1) j of a head
+ * becomes (x0 c - x1 s, x1 c + x0 s), c = mscale cos(a), s = mscale sin(a),
+ * a = position * inv_freq[j], with the angle, its cosine and sine and the
+ * rotation in 64 bits and one rounding at the end. */
+typedef struct kvs_rope {
+    const float* inv_freq; /* device [rot_dim / 2] */
+    int rot_dim;           /* even, 0..128; values from rot_dim on are kept as they are;
+                              0 = no rotation */
+    int interleaved;       /* pairs are (2j, 2j+1) if 1, (j, j + rot_dim/2) if 0 */
+    const int* positions;  /* device [n_rows], or NULL: own position + pos_offset */
+    int pos_offset;        /* e.g. the tokens of a shared prefix */
+    float mscale;          /* 0 = 1 */
+} kvs_rope;
+
+/* How scores are formed and which keys a row sees.  s = scale q.k; with a
+ * softcap c, s = c tanh(s / c); with slopes, s -= slope[head] |p - j| for a row
+ * at position p and key j (positions count the shared prefix first).  A row
+ * sees the keys first <= j < end that exist: first defaults to max(0, p -
+ * window + 1) (0 without a window), end to p + 1 (causal).  Given arrays
+ * replace these bounds: first_key the lower (then no window), end_key the
+ * upper, which makes document masks (first = the document's first key) and
+ * prefix masks (end past p + 1 inside a bidirectional part).  A row that sees
+ * no key gets out = 0 and lse = -inf.  Values of keys that a row does not see
+ * never count, whatever they hold. */
+typedef struct kvs_score {
+    float scale;               /* 0 = 1/sqrt(128) */
+    float softcap;             /* 0 = none; > 0 */
+    int window;                /* 0 = none; keys a row sees, itself included */
+    const float* alibi_slopes; /* device [n_q_heads] or NULL */
+    const int* first_key;      /* device [n_rows] or NULL */
+    const int* end_key;        /* device [n_rows] or NULL */
+} kvs_score;
+
+/* A prefix that every sequence of the batch shares: its tokens come before
+ * each sequence's own, and its pages are read once for all rows. */
+typedef struct kvs_page_prefix {
+    const int* page_table; /* device [pages of n_tokens] */
+    int n_tokens;          /* >= 0; need not end at a page boundary */
+} kvs_page_prefix;
+
+/* Rotate K (and Q), quantize K and V rows and write them to their pages.  k, v:
+ * dtype [n_rows][n_kv_heads][128]; K is rounded to binary32 after the rotation
+ * and then stored by the rules of kvs_append, V as it is.  q and q_out (dtype
+ * [n_rows][n_q_heads][128]) are both NULL or both given; q_out receives Q
+ * rotated, rounded to dtype, and may be q itself.  rope NULL = no rotation (Q
+ * is then copied).  dtype is KVS_DT_F16, KVS_DT_BF16 or KVS_DT_F32.  Two rows
+ * of a batch must not have the same page slot. */
+int kvs_append_pages(const kvs_page_pool* pool, const kvs_page_batch* batch, int dtype, const kvs_page_rows* k,
+                     const kvs_page_rows* v, int n_q_heads, const kvs_page_rows* q, const kvs_page_rows* q_out,
+                     const kvs_rope* rope, void* stream);
+
+/* The batch's rows read back from the pages as values d q (+ m), dtype
+ * [n_rows][n_kv_heads][128] (KVS_DT_F32 is exact, the others round once); k or
+ * v may be NULL.  A whole cache is a batch with as many rows as tokens.  Rows
+ * at negative positions get zeros. */
+int kvs_read_pages(const kvs_page_pool* pool, const kvs_page_batch* batch, int dtype, const kvs_page_rows* k,
+                   const kvs_page_rows* v, void* stream);
+
+/* Attention of the batch's rows over their sequences' pages, after the shared
+ * prefix if one is given.  q: q_dtype (F16 or BF16) [n_rows][n_q_heads][128];
+ * out: out_dtype (F16, BF16 or F32); lse fp32 [n_rows][n_q_heads] (natural
+ * log) or NULL; score and prefix may be NULL.  Products have 16-bit operands
+ * and fp32 accumulation, softmax statistics are fp32.  Up to 32 rows per kv
+ * head (rows of a sequence x n_q_heads / n_kv_heads) the probabilities go in
+ * as two 16-bit terms unless out is BF16, so that an F32 or F16 result has
+ * fp32-class accuracy with every V type but Q4_1 and Q5_1 (whose values are
+ * rounded to fp16); wider rows use the tcgen05 tensor cores with K, V and
+ * probabilities rounded to fp16 once each.
+ *
+ * workspace: device, 256-byte aligned, at least kvs_attend_pages_workspace
+ * bytes, zero-filled once before its first use; every call leaves it ready for
+ * the next.  Calls that share a workspace must be ordered (one stream, or
+ * events): two calls at once, or two captured graphs replayed at once, need a
+ * workspace each. */
+int kvs_attend_pages(const kvs_page_pool* pool, const kvs_page_batch* batch, int q_dtype, int n_q_heads,
+                     const kvs_page_rows* q, int out_dtype, const kvs_page_rows* out, float* lse,
+                     const kvs_score* score, const kvs_page_prefix* prefix, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/* Pure host: workspace bytes for any kvs_attend_pages call with at most this
+ * batch's n_seqs and n_rows and these heads; 0 if an argument is bad. */
+size_t kvs_attend_pages_workspace(const kvs_page_batch* batch, int n_q_heads, int n_kv_heads);
+
 /* Failure-detection self-test: launch one GPU thread that waits, through the
  * same bounded mbarrier wait every libkvs kernel uses, on a barrier phase that
  * nothing completes.  The wait gives up after limit_s seconds (0 < limit_s <=
  * 10) and records KVS_ERR_WAIT_TIMEOUT in the error word, which is returned in
  * *err_bits; the device stays usable.  Needs no handle. */
 #define KVS_ERR_WAIT_TIMEOUT 1
+#define KVS_ERR_BAD_PAGE     2 /* a page number outside the pool (kvs_page_batch.status) */
 int kvs_selftest_bounded_wait(int device, double limit_s, int* err_bits);
 
 /* Last error text of the handle (or of the calling thread's last failed
