@@ -45,7 +45,7 @@ POOLS = [(dict(pages=None), "null pool"), (dict(pages=A + 8), "16-byte"), (dict(
 BATCHES = [(dict(n_seqs=-1), "negative"), (dict(n_rows=-1), "negative"), (dict(table_stride=-1), "negative"), (dict(max_new=-2), "negative"),
            (dict(q_start=None), "null q_start"), (dict(seq_len=None), "null q_start"), (dict(page_table=None), "null page_table"),
            (dict(q_start=A + 2), "4-byte"), (dict(status=A + 1), "4-byte"), (dict(page_table=A + 3), "4-byte")]
-ROWS = [(dict(data=None), "null"), (dict(data=A + 8), "16 bytes"), (dict(row=516), "16 bytes"), (dict(head=132), "16 bytes")]
+ROWS = [(dict(data=None), "null"), (dict(data=A + 8), "16 bytes"), (dict(row=514), "16 bytes"), (dict(head=130), "16 bytes")]
 
 
 @pytest.mark.parametrize("what,text", POOLS + BATCHES)
