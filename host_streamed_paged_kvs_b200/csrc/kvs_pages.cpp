@@ -130,12 +130,16 @@ int launched(cudaError_t e) { return e == cudaSuccess ? KVS_OK : fail(KVS_E_CUDA
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// the workspace: arrival counters, records of shared units, the prefix's records
+// the workspace: arrival counters, the many-row kernel's plan, records of shared
+// units (both kernels' in turn), the prefix's records
 struct Workspace {
-    size_t counters = 0, records, prior_acc, prior_ml, bytes;
-    Workspace(long long n_rows, long long n_qh) {
-        records = up256((size_t)kFewCtas * sizeof(int));
-        prior_acc = records + up256(kFewRecordBytes);
+    size_t counters = 0, plan, units, records, prior_acc, prior_ml, bytes;
+    Workspace(long long n_rows, long long n_seqs, long long n_qh, int group) {
+        const bool wide = n_rows * group > kFewRowsMax;
+        plan = up256((size_t)kFewCtas * sizeof(int));
+        units = plan + up256(sizeof(WidePlan));
+        records = units + (wide ? up256((size_t)wide_groups(n_rows, group, n_seqs) * sizeof(WideUnit)) : 0);
+        prior_acc = records + up256(wide && kWideRecordBytes > kFewRecordBytes ? kWideRecordBytes : kFewRecordBytes);
         prior_ml = prior_acc + up256((size_t)n_rows * n_qh * kHeadDim * sizeof(float));
         bytes = prior_ml + up256((size_t)n_rows * n_qh * sizeof(float2));
     }
@@ -194,11 +198,11 @@ extern "C" int kvs_read_pages(const kvs_page_pool* pool, const kvs_page_batch* b
 }
 
 extern "C" size_t kvs_attend_pages_workspace(const kvs_page_batch* batch, int n_q_heads, int n_kv_heads) {
-    if (!batch || batch->n_rows < 0 || n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads) {
+    if (!batch || batch->n_rows < 0 || batch->n_seqs < 0 || n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads) {
         set_last_error("kvs_attend_pages_workspace: bad argument");
         return 0;
     }
-    return Workspace(batch->n_rows, n_q_heads).bytes;
+    return Workspace(batch->n_rows, batch->n_seqs, n_q_heads, n_q_heads / n_kv_heads).bytes;
 }
 
 extern "C" int kvs_attend_pages(const kvs_page_pool* pool, const kvs_page_batch* batch, int q_dtype, int n_q_heads,
@@ -223,12 +227,14 @@ extern "C" int kvs_attend_pages(const kvs_page_pool* pool, const kvs_page_batch*
     a.lse = lse;
     a.scale = 0.08838834764831845f;  // 1/sqrt(128)
     if (score) {
-        if (!std::isfinite(score->scale) || !std::isfinite(score->softcap) || score->softcap < 0.0f || score->window < 0)
+        if (!std::isfinite(score->scale) || !std::isfinite(score->softcap) || score->softcap < 0.0f || score->window < 0 ||
+            (score->softcap > 0.0f && !std::isfinite(1.0f / score->softcap)))
             return fail(KVS_E_INVAL, "score: scale and softcap must be finite, softcap and window not negative");
         if (!aligned(score->alibi_slopes, 4) || !aligned(score->first_key, 4) || !aligned(score->end_key, 4))
             return fail(KVS_E_INVAL, "score arrays must be 4-byte aligned");
         if (score->scale != 0.0f) a.scale = score->scale;
         a.softcap = score->softcap;
+        a.inv_cap = a.softcap > 0.0f ? 1.0f / a.softcap : 0.0f;
         a.window = score->window;
         a.slopes = score->alibi_slopes;
         a.first_key = score->first_key;
@@ -240,11 +246,13 @@ extern "C" int kvs_attend_pages(const kvs_page_pool* pool, const kvs_page_batch*
         a.prefix_table = prefix->page_table;
         a.prefix_len = prefix->n_tokens;
     }
-    const Workspace w(a.batch.n_rows, n_q_heads);
+    const Workspace w(a.batch.n_rows, a.batch.n_seqs, n_q_heads, a.group);
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < w.bytes)
         return fail(KVS_E_INVAL, "workspace: null, not 256-byte aligned, or smaller than kvs_attend_pages_workspace says");
     uint8_t* base = static_cast<uint8_t*>(workspace);
     a.counters = reinterpret_cast<int*>(base + w.counters);
+    a.plan = reinterpret_cast<WidePlan*>(base + w.plan);
+    a.units = reinterpret_cast<WideUnit*>(base + w.units);
     a.records = reinterpret_cast<float*>(base + w.records);
     a.prior_acc = reinterpret_cast<float*>(base + w.prior_acc);
     a.prior_ml = reinterpret_cast<float2*>(base + w.prior_ml);
@@ -258,12 +266,25 @@ extern "C" int kvs_attend_pages(const kvs_page_pool* pool, const kvs_page_batch*
         return fail(KVS_E_CUDA, "cuTensorMapEncodeTiled failed");
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int n_sms = on.n_sms();
-    auto unit_rows = [](long long rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : kFewRowsMax); };
+    // Up to 32 rows per kv head go to the few-row kernel (HBM bound, fp32-class
+    // sums), more to the tensor-core kernel.
+    auto few = [&](AttendPagesArgs& x, long long rows) {
+        return launched(launch_attend_few(x, maps, rows <= 8 ? 8 : (rows <= 16 ? 16 : kFewRowsMax), n_sms, s));
+    };
+    const long long all = (long long)a.batch.n_rows * a.group;
     if (a.prefix_len > 0) {
         AttendPagesArgs p = a;
         p.prefix_phase = 1;
-        if ((rc = launched(launch_attend_few(p, maps, unit_rows((long long)a.batch.n_rows * a.group), n_sms, s))) != KVS_OK) return rc;
+        rc = all > kFewRowsMax ? launched(launch_attend_wide(p, maps, n_sms, s)) : few(p, all);
+        if (rc != KVS_OK) return rc;
     }
-    const long long most = batch->max_new > 0 && batch->max_new < a.batch.n_rows ? batch->max_new : a.batch.n_rows;
-    return launched(launch_attend_few(a, maps, unit_rows(most * a.group), n_sms, s));
+    const long long most = (batch->max_new > 0 && batch->max_new < a.batch.n_rows ? batch->max_new : a.batch.n_rows) * (long long)a.group;
+    if (most <= kFewRowsMax) {
+        a.few_rows = 0x7fffffff;
+        return few(a, most);
+    }
+    a.few_rows = a.batch.n_seqs == 1 ? 0 : kFewRowsMax;
+    rc = launched(launch_attend_wide(a, maps, n_sms, s));
+    if (rc == KVS_OK && a.few_rows > 0) rc = few(a, 8);
+    return rc;
 }

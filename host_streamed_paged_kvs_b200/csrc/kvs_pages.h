@@ -63,6 +63,7 @@ struct AttendPagesArgs {
     int q_dtype, out_dtype;
     float* lse;              // [n_rows][n_qh] or null
     float scale, softcap;    // natural units; softcap 0 = none
+    float inv_cap;           // 1 / softcap
     int window;
     const float* slopes;
     const int* first_key;
@@ -75,7 +76,31 @@ struct AttendPagesArgs {
     float2* prior_ml;        // [n_rows][n_qh] (ref, sum)
     float* records;          // pieces of units that several CTAs share
     int* counters;           // arrivals at such a unit, zero between calls
+    int few_rows;            // own phase: sequences with more rows per kv head than this belong
+                             // to the many-row kernel, the others to the few-row one
+    struct WideUnit* units;  // the many-row kernel's list, made on the device for each call
+    struct WidePlan* plan;
 };
+
+// One row group (up to 256 rows of a sequence, or of the batch) and the 128-key
+// stages it needs; each kv head has a unit of it.
+struct WideUnit {
+    int seq, row0, rows;     // rows row0 .. row0 + rows - 1 of the sequence, token-major
+    int stage0, n_stages;    // at least 1
+    int n_keys;              // keys that exist
+    long long before;        // stages of the groups before this one
+};
+struct WidePlan {
+    int n_groups, pad;
+    long long total;         // stages of all groups
+};
+constexpr int kWideRows = 256;
+constexpr int kWideCtas = 148;
+constexpr size_t kWideRecordBytes = (size_t)kWideCtas * 2 * kWideRows * 132 * 4;
+// groups of a batch: full ones and one ragged end per sequence
+inline long long wide_groups(long long n_rows, int group, long long n_seqs) {
+    return n_rows * group / kWideRows + n_seqs + 1;
+}
 
 // rows of a unit of the few-row kernel: 8, 16 or 32
 constexpr int kFewRowsMax = 32;
@@ -88,6 +113,8 @@ struct PageMaps {
 };
 
 cudaError_t launch_attend_few(const AttendPagesArgs& a, const PageMaps& maps, int unit_rows, int n_sms, cudaStream_t s);
+
+cudaError_t launch_attend_wide(const AttendPagesArgs& a, const PageMaps& maps, int n_sms, cudaStream_t s);
 
 cudaError_t launch_append_pages(const AppendPagesArgs& a, int dtype, int n_sms, cudaStream_t s);
 cudaError_t launch_read_pages(const ReadPagesArgs& a, int dtype, int n_sms, cudaStream_t s);
@@ -154,17 +181,14 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// tanh to 1e-7 absolute: an odd polynomial (the Taylor series to x^9) below 1/4,
-// where 1 - 2 / (e^2x + 1) would lose its leading digits, that form above
-__device__ __forceinline__ float tanh_exact(float x) {
-    const float y = x * x;
-    const float small = x * fmaf(y, fmaf(y, fmaf(y, fmaf(y, 62.0f / 2835.0f, -17.0f / 315.0f), 2.0f / 15.0f), -1.0f / 3.0f), 1.0f);
-    const float big = 1.0f - __fdividef(2.0f, exp2_fast(x * 2.8853900817779268f) + 1.0f);
-    return fabsf(x) < 0.25f ? small : big;
+// tanh as 1 - 2 / (e^2x + 1): 3 * 2^-23 absolute, so a capped score is off by
+// at most 4e-7 of its cap
+__device__ __forceinline__ float tanh_abs(float x) {
+    return 1.0f - __fdividef(2.0f, exp2_fast(x * 2.8853900817779268f) + 1.0f);
 }
 // score of one key in the log2 domain from the product q.k times scale
 __device__ __forceinline__ float score_log2(const AttendPagesArgs& a, float s, float slope, int pos, int key) {
-    if (a.softcap > 0.0f) s = a.softcap * tanh_exact(s / a.softcap);
+    if (a.softcap > 0.0f) s = a.softcap * tanh_abs(s * a.inv_cap);
     return (s - slope * fabsf((float)(pos - key))) * 1.4426950408889634f;
 }
 #endif

@@ -167,7 +167,8 @@ __device__ __forceinline__ Seq seq_of(const AttendPagesArgs& a, int i) {
         s.stage0 = 0;
     } else {
         s.row0 = b.q_start[i];
-        s.rows = max(0, b.q_start[i + 1] - s.row0);
+        s.rows = min(max(0, b.q_start[i + 1] - s.row0), b.n_rows);
+        if ((long long)s.rows * a.group > a.few_rows) s.rows = 0;  // the many-row kernel's
         const long long most = (long long)b.table_stride * kPageTokens;
         s.n_keys = max(0, b.seq_len[i]);
         keys = (int)min((long long)s.n_keys, most);
@@ -780,9 +781,31 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
             if (lane == 0) arrive(&empty[buf]);
         }
 
-        // ---- the piece's end: join the warps, 8 rows at a time ----
+        // ---- the piece's end ----
         const bool bad = p.bad;
         if (bad && tid == 0 && a.batch.status) atomicOr(a.batch.status, kErrBadPage);
+        // joins the four warps' sums of rows 8 nt .. + 7 from the join buffer; two rows a
+        // warp, lane = dims 4 lane .. + 3
+        auto join_warps = [&](int nt, bool record) {
+#pragma unroll
+            for (int rr = 0; rr < 2; ++rr) {
+                const int r = warp + kConsumers * rr, pr = 8 * nt + r;
+                if (pr >= p.rows || p.token[pr] < 0) continue;
+                float M = -CUDART_INF_F, L = 0.0f;
+                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int w = 0; w < kConsumers; ++w)
+                    join(acc, M, L, *reinterpret_cast<const float4*>(red + (w * 8 + r) * kRedRow + 4 * lane), sml[(w * 8 + r) * 2],
+                         sml[(w * 8 + r) * 2 + 1]);
+                if (!record) {
+                    finish_row<VT, KT>(a, p.seq, p.token[pr], p.head[pr], acc, M, L);
+                } else {
+                    float* rec = a.records + ((size_t)(blockIdx.x * 2 + p.slot) * kFewRowsMax + pr) * kRecordFloats;
+                    *reinterpret_cast<float4*>(rec + 4 * lane) = acc;
+                    if (lane == 0) *reinterpret_cast<float2*>(rec + 128) = make_float2(M, L);
+                }
+            }
+        };
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             if (8 * nt >= p.rows) break;  // uniform
@@ -808,28 +831,12 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                 }
             }
             if (!consumers_sync()) return;
-#pragma unroll
-            for (int rr = 0; rr < 2; ++rr) {
-                const int r = warp + kConsumers * rr, pr = 8 * nt + r;
-                if (pr >= p.rows || p.token[pr] < 0) continue;
-                float M = -CUDART_INF_F, L = 0.0f;
-                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                for (int w = 0; w < kConsumers; ++w)
-                    join(acc, M, L, *reinterpret_cast<const float4*>(red + (w * 8 + r) * kRedRow + 4 * lane), sml[(w * 8 + r) * 2],
-                         sml[(w * 8 + r) * 2 + 1]);
-                if (p.slot < 0) {
-                    finish_row<VT, KT>(a, p.seq, p.token[pr], p.head[pr], acc, M, L);
-                } else {
-                    float* rec = a.records + ((size_t)(blockIdx.x * 2 + p.slot) * kFewRowsMax + pr) * kRecordFloats;
-                    *reinterpret_cast<float4*>(rec + 4 * lane) = acc;
-                    if (lane == 0) *reinterpret_cast<float2*>(rec + 128) = make_float2(M, L);
-                }
-            }
+            join_warps(nt, p.slot >= 0);
             if (!consumers_sync()) return;
         }
         if (p.slot >= 0) {
-            // ---- a shared unit: the last CTA to arrive joins the records ----
+            // ---- a shared unit: the last CTA to arrive joins the records.  Each warp
+            // takes every fourth record, two rows and eight records in flight ----
             __threadfence();
             if (!consumers_sync()) return;
             if (tid == 0) {
@@ -841,29 +848,57 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
             if (!consumers_sync()) return;
             if (*sLast) {
                 __threadfence();
-                for (int pr = warp; pr < p.rows; pr += kConsumers) {
-                    if (p.token[pr] < 0) continue;
-                    // the first CTA began the unit, the others continue it
-                    auto record = [&](int c) {
-                        return a.records + ((size_t)((p.cta0 + c) * 2 + (c == 0 ? 1 : 0)) * kFewRowsMax + pr) * kRecordFloats;
-                    };
-                    float M = -CUDART_INF_F, L = 0.0f;
-                    for (int c = lane; c < p.n_ctas; c += 32) M = fmaxf(M, __ldcg(record(c) + 128));
+                const int n = p.n_ctas, cta0 = p.cta0, rows = p.rows;
+                constexpr int kBatch = 8;
+#pragma unroll 1
+                for (int nt = 0; 8 * nt < rows; ++nt) {
+#pragma unroll 1
+                    for (int r0 = 0; r0 < 8 && 8 * nt + r0 < rows; r0 += 2) {
+                        float4 acc[2];
+                        float M[2], L[2];
 #pragma unroll
-                    for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-                    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-                    for (int c = 0; c < p.n_ctas; ++c) {
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(record(c)) + lane);
-                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(record(c) + 128));
-                        const float w = ml.x == M ? 1.0f : exp2_fast(ml.x - M);
-                        acc.x = fmaf(v.x, w, acc.x);
-                        acc.y = fmaf(v.y, w, acc.y);
-                        acc.z = fmaf(v.z, w, acc.z);
-                        acc.w = fmaf(v.w, w, acc.w);
-                        L = fmaf(ml.y, w, L);
+                        for (int k = 0; k < 2; ++k) {
+                            acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            M[k] = -CUDART_INF_F;
+                            L[k] = 0.0f;
+                        }
+#pragma unroll 1
+                        for (int c0 = warp; c0 < n; c0 += kConsumers * kBatch) {
+                            float4 v[kBatch][2];
+                            float2 ml[kBatch][2];
+#pragma unroll
+                            for (int b = 0; b < kBatch; ++b) {
+                                const int c = c0 + kConsumers * b;
+                                // the first CTA began the unit, the others continue it
+                                const float* rec = a.records +
+                                    ((size_t)((cta0 + min(c, n - 1)) * 2 + (c == 0 ? 1 : 0)) * kFewRowsMax + 8 * nt + r0) * kRecordFloats;
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    v[b][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                                    ml[b][k] = make_float2(-CUDART_INF_F, 0.0f);
+                                    if (c < n && 8 * nt + r0 + k < rows) {
+                                        v[b][k] = __ldcg(reinterpret_cast<const float4*>(rec + k * kRecordFloats) + lane);
+                                        ml[b][k] = __ldcg(reinterpret_cast<const float2*>(rec + k * kRecordFloats + 128));
+                                    }
+                                }
+                            }
+#pragma unroll
+                            for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) join(acc[k], M[k], L[k], v[b][k], ml[b][k].x, ml[b][k].y);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            *reinterpret_cast<float4*>(red + (warp * 8 + r0 + k) * kRedRow + 4 * lane) = acc[k];
+                            if (lane == 0) {
+                                sml[(warp * 8 + r0 + k) * 2] = M[k];
+                                sml[(warp * 8 + r0 + k) * 2 + 1] = L[k];
+                            }
+                        }
                     }
-                    finish_row<VT, KT>(a, p.seq, p.token[pr], p.head[pr], acc, M, L);
+                    if (!consumers_sync()) return;
+                    join_warps(nt, false);
+                    if (!consumers_sync()) return;
                 }
             }
         }

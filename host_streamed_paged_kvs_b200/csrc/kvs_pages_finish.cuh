@@ -103,6 +103,24 @@ __device__ __noinline__ float4 slow_row(const AttendPagesArgs& a, int seq, int r
     return make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
 }
 
+// four values of a row of the result
+__device__ __forceinline__ void store_out4(const AttendPagesArgs& a, int row, int head, int d, const float4& o) {
+    const long long to = row * a.out.row + head * a.out.head + d;
+    if (a.out_dtype == kDtF32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out.p) + to) = o;
+        return;
+    }
+    uint2 w;
+    if (a.out_dtype == kDtF16) {
+        *reinterpret_cast<__half2*>(&w.x) = __floats2half2_rn(o.x, o.y);
+        *reinterpret_cast<__half2*>(&w.y) = __floats2half2_rn(o.z, o.w);
+    } else {
+        *reinterpret_cast<__nv_bfloat162*>(&w.x) = __floats2bfloat162_rn(o.x, o.y);
+        *reinterpret_cast<__nv_bfloat162*>(&w.y) = __floats2bfloat162_rn(o.z, o.w);
+    }
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out.p) + to) = w;
+}
+
 // (acc, M, L) += (b, m, l): records relative to 2^M and 2^m
 __device__ __forceinline__ void join(float4& acc, float& M, float& L, const float4& b, float m, float l) {
     const float top = fmaxf(M, m);
@@ -139,20 +157,7 @@ __device__ __forceinline__ void finish_row(const AttendPagesArgs& a, int seq, in
         const bool bad = !((acc.x + acc.y + acc.z + acc.w) * 0.0f == 0.0f);
         if (__any_sync(0xffffffffu, bad) && L * 0.0f == 0.0f) o = slow_row<VT, KT>(a, seq, row, head);
     }
-    const long long to = row * a.out.row + head * a.out.head + 4 * lane;
-    if (a.out_dtype == kDtF32) {
-        *reinterpret_cast<float4*>(static_cast<float*>(a.out.p) + to) = o;
-    } else {
-        uint2 w;
-        if (a.out_dtype == kDtF16) {
-            *reinterpret_cast<__half2*>(&w.x) = __floats2half2_rn(o.x, o.y);
-            *reinterpret_cast<__half2*>(&w.y) = __floats2half2_rn(o.z, o.w);
-        } else {
-            *reinterpret_cast<__nv_bfloat162*>(&w.x) = __floats2bfloat162_rn(o.x, o.y);
-            *reinterpret_cast<__nv_bfloat162*>(&w.y) = __floats2bfloat162_rn(o.z, o.w);
-        }
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out.p) + to) = w;
-    }
+    store_out4(a, row, head, 4 * lane, o);
     if (a.lse && lane == 0) a.lse[at] = L == 0.0f ? -CUDART_INF_F : (M + log2f(L)) * 0.69314718055994531f;
 }
 

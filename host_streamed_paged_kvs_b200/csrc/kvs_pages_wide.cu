@@ -1,0 +1,949 @@
+// kvs_pages_wide.cu -- attention of many rows per kv head over quantized pages
+// found through page tables, on the tcgen05 tensor cores (kvs_attend_pages:
+// prompt chunks, and a prefix that many sequences share).
+//
+// What bounds it: the tensor cores.  Every (row, key) pair costs 512 flops; 256
+// rows against 128 keys are 16.8 MFLOP, 2,050 cycles of an SM at the dense rate
+// (2,400 at the rate that N = 128 instructions reach), beside 2,050 cycles of
+// exponentials (16 a cycle) and the conversion of 32,768 codes.
+//
+// A unit is (row group of 256 rows, kv head): two 128-row tiles that share every
+// converted stage of 128 keys.  A planning launch finds each group's stages
+// (causal bounds, windows and key intervals cut them) on the device; all units'
+// stages form one list and every CTA takes an equal run of it.  Units that
+// several CTAs share leave records, which a last launch joins in CTA order.
+//
+// Roles, handing work over by mbarriers only, 12 warps (3 a sub-partition, so
+// that each may have 168 registers):
+//   warps 0..3, 4..7: softmax of tile 0 and 1, a thread a row.  S comes out of
+//     tensor memory 64 columns at a time; weights 2^(s - r) are formed with the
+//     row's kept reference, packed to fp16 and put back over S.  A row's maximum
+//     is taken only when its weights' sum says that the reference is too low
+//     (over 2^13, or the first keys seen): then the row of O is rescaled.
+//   warps 8..10: convert K and V of each stage to fp16 operand tiles (128-byte
+//     swizzle); the next stage's codes are in registers while they wait.
+//     fp16 rows come by TMA instead, as they are.
+//   warp 11: one thread issues S = Q K^T and O += P V of the two tiles in turn,
+//     so that one tile's softmax runs under the other's products.
+// K and V are rounded to fp16 once (d q), the weights once; sums and softmax
+// statistics are fp32.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math_constants.h>
+
+#include <algorithm>
+#include <atomic>
+#include <climits>
+
+#include "kvs_pages.h"
+#include "kvs_pages_finish.cuh"
+#include "kvs_ptx.cuh"
+
+namespace kvs {
+namespace {
+
+constexpr int kSoftWarps = 8, kProdWarps = 3, kMmaWarp = kSoftWarps + kProdWarps;
+constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kStageKeys = 128;
+constexpr int kTileBytes = 128 * kHeadDim * 2;        // 32 KB: an operand of 128 rows x 128 fp16
+constexpr int kBufs = 2;
+constexpr int kOffQ = 0;                              // [tile]
+constexpr int kOffK = 2 * kTileBytes;                 // [buffer]
+constexpr int kOffV = kOffK + kBufs * kTileBytes;
+constexpr int kOffBar = kOffV + kBufs * kTileBytes;
+constexpr size_t kSmem = 1024 + kOffBar + 256;
+static_assert(kSmem <= 232448, "shared memory");
+constexpr uint64_t kWaitNs = 10000000000ull;          // leaves room for rows recomputed the slow way
+constexpr float kSumMost = 8192.0f;                   // a row's weights of one stage: fp16 holds each
+constexpr uint32_t kColS = 0, kColO = 256;            // tensor memory columns, + 128 per tile
+// f16 x f16 -> f32, M = N = 128, A K-major (Q) or from tensor memory (P); B K-major (K), MN-major (V)
+constexpr uint32_t kIdescS = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+constexpr uint32_t kIdescPV = kIdescS | (1u << 16);
+
+// shared-memory matrix descriptor (version 1, 128-byte swizzle): rows of 128
+// bytes in groups of 8, 64-column halves 16 KB apart
+__device__ __forceinline__ uint64_t smem_desc(uint32_t start, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((start >> 4) & 0x3FFF) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16) | ((uint64_t)((sbo >> 4) & 0x3FFF) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ uint64_t desc_k(uint32_t base, int kk) {  // dims 16 kk ..
+    return smem_desc(base + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t base, int kk) {  // keys 16 kk ..
+    return smem_desc(base + kk * 2048, 16384, 1024);
+}
+// byte offset of the 16-byte chunk (8 columns) c of a row
+__device__ __forceinline__ uint32_t chunk_off(int row, int c) {
+    return (uint32_t)((c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+__device__ __forceinline__ uint32_t h2u(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tma4(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ unsigned long long f2_bits(float a, float b) {
+    return (unsigned long long)__float_as_uint(a) | ((unsigned long long)__float_as_uint(b) << 32);
+}
+// packed pairs of fp32: a * b + c, a + b
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(f2_bits(a.x, a.y)), "l"(f2_bits(b.x, b.y)), "l"(f2_bits(c.x, c.y)));
+    return make_float2(__uint_as_float((uint32_t)r), __uint_as_float((uint32_t)(r >> 32)));
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a.x, a.y)), "l"(f2_bits(b.x, b.y)));
+    return make_float2(__uint_as_float((uint32_t)r), __uint_as_float((uint32_t)(r >> 32)));
+}
+__device__ __forceinline__ void st_chunk(uint8_t* tile, int row, int c, uint4 v) {
+    *reinterpret_cast<uint4*>(tile + chunk_off(row, c)) = v;
+}
+
+// ---- planning: the groups and the stages that their rows need ----
+constexpr int kPlanThreads = 1024;
+
+// this phase's sequence i: rows (tokens) and keys
+__device__ __forceinline__ void phase_seq(const AttendPagesArgs& a, int i, int& first_token, int& tokens, int& n_keys) {
+    const PageBatch& b = a.batch;
+    if (a.prefix_phase) {
+        first_token = 0;
+        tokens = max(0, min(b.n_rows, b.q_start[b.n_seqs]));
+        n_keys = a.prefix_len;
+    } else {
+        first_token = b.q_start[i];
+        tokens = min(max(0, b.q_start[i + 1] - first_token), b.n_rows);
+        if ((long long)tokens * a.group <= a.few_rows) tokens = 0;  // the other kernel's
+        n_keys = max(0, b.seq_len[i]);
+    }
+}
+
+__device__ __forceinline__ long long block_scan(long long v, long long* sums, long long& all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v += u;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = v;
+    __syncthreads();
+    all = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w < warp) v += sums[w];
+        all += sums[w];
+    }
+    return v;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) wide_plan_kernel(const __grid_constant__ AttendPagesArgs a, int max_groups) {
+    __shared__ long long sums[32];
+    __shared__ int sUpto[kPlanThreads], sTokens[kPlanThreads];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n_seqs = a.prefix_phase ? 1 : a.batch.n_seqs;
+    int n_groups = 0;
+    for (int i0 = 0; i0 < n_seqs; i0 += kPlanThreads) {
+        const int i = i0 + tid;
+        int first_token = 0, tokens = 0, n_keys = 0;
+        if (i < n_seqs) phase_seq(a, i, first_token, tokens, n_keys);
+        const int mine = (int)(((long long)tokens * a.group + kWideRows - 1) / kWideRows);
+        long long all;
+        const long long upto = block_scan(mine, sums, all);
+        sUpto[tid] = (int)upto;
+        sTokens[tid] = tokens;
+        __syncthreads();
+        // a warp per group
+        for (int g = warp; g < (int)all; g += kPlanThreads / 32) {
+            int lo = 0, hi = kPlanThreads - 1;  // the first thread whose sum passes g
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (sUpto[mid] > g) hi = mid; else lo = mid + 1;
+            }
+            if (n_groups + g >= max_groups) break;  // a malformed batch whose ranges overlap
+            int ft, tk, keys;
+            phase_seq(a, i0 + lo, ft, tk, keys);
+            const int before = lo > 0 ? sUpto[lo - 1] : 0;
+            WideUnit u;
+            u.seq = i0 + lo;
+            u.row0 = (g - before) * kWideRows;
+            u.rows = min(kWideRows, sTokens[lo] * a.group - u.row0);
+            u.n_keys = keys;
+            u.before = 0;
+            const int t0 = ft + u.row0 / a.group, t1 = ft + (u.row0 + u.rows - 1) / a.group;
+            const int shift = a.prefix_phase ? 0 : a.prefix_len;
+            int from = INT_MAX, to = 0;
+            for (int t = t0 + lane; t <= t1; t += 32) {
+                if ((unsigned)t >= (unsigned)a.batch.n_rows) continue;
+                const int of = a.prefix_phase ? find_seq_thread(a.batch, t) : u.seq;
+                if (of < 0) continue;
+                const RowView v = row_view(a, of, t);
+                const int f = max(v.first - shift, 0), e = min(v.end - shift, keys);
+                if (f < e) {
+                    from = min(from, f);
+                    to = max(to, e);
+                }
+            }
+#pragma unroll
+            for (int off = 16; off; off >>= 1) {
+                from = min(from, __shfl_xor_sync(0xffffffffu, from, off));
+                to = max(to, __shfl_xor_sync(0xffffffffu, to, off));
+            }
+            // keys beyond the page table are nobody's: such a unit comes out as NaN
+            if (!a.prefix_phase) to = (int)min((long long)to, (long long)a.batch.table_stride * kPageTokens);
+            u.stage0 = from < to ? from / kStageKeys : 0;
+            u.n_stages = from < to ? (to + kStageKeys - 1) / kStageKeys - u.stage0 : 1;
+            if (lane == 0) a.units[n_groups + g] = u;
+        }
+        n_groups = min(n_groups + (int)all, max_groups);
+        __syncthreads();
+    }
+    long long total = 0;
+    for (int g0 = 0; g0 < n_groups; g0 += kPlanThreads) {
+        const int g = g0 + tid;
+        const int n = g < n_groups ? a.units[g].n_stages : 0;
+        long long all;
+        const long long upto = block_scan(n, sums, all);
+        if (g < n_groups) a.units[g].before = total + upto - n;
+        total += all;
+    }
+    if (tid == 0) {
+        a.plan->n_groups = n_groups;
+        a.plan->total = total;
+    }
+}
+
+// A CTA's (or a join's) way through the list.  Position x of the list of
+// n_kv * total stages lies in group g with n_kv * before_g <= x.
+struct Walk {
+    WideUnit u;
+    int group, h;             // group and kv head of the current unit
+    long long unit0;          // list position of the unit's first stage
+};
+__device__ __forceinline__ bool walk_to(const AttendPagesArgs& a, Walk& w, long long x, int n_groups) {
+    const int n_kv = a.pool.n_kv;
+    while (x >= n_kv * (w.u.before + w.u.n_stages)) {
+        if (++w.group >= n_groups) return false;
+        w.u = a.units[w.group];
+    }
+    w.h = (int)((x - n_kv * w.u.before) / w.u.n_stages);
+    w.unit0 = n_kv * w.u.before + (long long)w.h * w.u.n_stages;
+    return true;
+}
+// by a whole warp: the group of list position x
+__device__ __forceinline__ int find_group(const AttendPagesArgs& a, long long x, int n_groups) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = n_groups;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
+        const bool le = at < hi && a.pool.n_kv * a.units[at].before <= x;
+        const int n = __popc(__ballot_sync(0xffffffffu, le));
+        lo += n * step;
+        hi = min(hi, lo + step);
+    }
+    return lo;
+}
+
+// a producer warp's loads of a stage: 128-byte rows 4 a load, 64-byte rows 8 a load
+constexpr int kMine128 = (32 + kProdWarps - 1) / kProdWarps, kMine64 = (16 + kProdWarps - 1) / kProdWarps;
+
+// 16 int8 codes times d as two 16-byte chunks
+__device__ __forceinline__ void conv_s8(const uint4& c, uint32_t d2, uint4& lo, uint4& hi) {
+    const __half2 b = __float2half2_rn(1152.0f), d = u2h(d2);
+    auto four = [&](uint32_t w, uint32_t& x, uint32_t& y) {
+        w ^= 0x80808080u;
+        x = h2u(__hmul2(__hsub2(u2h(__byte_perm(w, 0x64646464u, 0x4140)), b), d));
+        y = h2u(__hmul2(__hsub2(u2h(__byte_perm(w, 0x64646464u, 0x4342)), b), d));
+    };
+    four(c.x, lo.x, lo.y);
+    four(c.y, lo.z, lo.w);
+    four(c.z, hi.x, hi.y);
+    four(c.w, hi.z, hi.w);
+}
+
+template <int VT, int KT>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_wide_kernel(const __grid_constant__ AttendPagesArgs a, const __grid_constant__ PageMaps maps) {
+    using PG = PageGeom<VT, KT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
+    uint64_t* k_full = bars;        // [buffer] K written (a producer warp each; TMA for fp16 K)
+    uint64_t* k_free = bars + 2;    // [buffer] every S product that reads it is complete
+    uint64_t* v_full = bars + 4;
+    uint64_t* v_free = bars + 6;
+    uint64_t* v_raw = bars + 8;     // [buffer] fp16 V landed
+    uint64_t* s_full = bars + 10;   // [tile] S complete
+    uint64_t* p_full = bars + 12;   // [tile] weights written
+    uint64_t* o_full = bars + 14;   // [tile] the piece's last product complete
+    uint64_t* q_full = bars + 16;   // [tile] Q written
+    uint64_t* done = bars + 18;     // every product complete
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19);
+    int* sGroup = reinterpret_cast<int*>(tmem_slot + 1);
+    volatile int* sAbort = reinterpret_cast<volatile int*>(sGroup + 1);
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n_kv = a.pool.n_kv;
+    if (warp == 0) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    if (tid == 32) {
+        *sAbort = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&k_full[i], KT == kKF16 ? 1 : kProdWarps);
+            mbar_init(&k_free[i], 1);
+            mbar_init(&v_full[i], kProdWarps);
+            mbar_init(&v_free[i], 1);
+            mbar_init(&v_raw[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&o_full[i], 1);
+            mbar_init(&q_full[i], 4);
+        }
+        mbar_init(done, 1);
+        fence_mbar_init();
+    }
+    const int n_groups = a.plan->n_groups;
+    const long long total = a.plan->total * n_kv;
+    const long long per = max(1ll, (total + gridDim.x - 1) / gridDim.x);
+    const long long run0 = min(total, per * blockIdx.x), run1 = min(total, run0 + per);
+    if (warp == 2 && run0 < run1) {
+        const int g = find_group(a, run0, n_groups);
+        if (lane == 0) *sGroup = g;
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    bool ok = run0 < run1;
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {  // by one thread or a whole warp
+        if (!ok || *sAbort) return ok = false;
+        if (!mbar_wait_bounded(bar, parity, a.batch.status, kWaitNs)) {
+            ok = false;
+            *sAbort = 1;
+        }
+        return ok;
+    };
+    Walk w;
+    w.group = ok ? *sGroup : 0;
+    if (ok) w.u = a.units[w.group];
+    const int shift = a.prefix_phase ? 0 : a.prefix_len;
+
+    if (warp < kSoftWarps) {
+        // ============================ softmax ============================
+        const int tile = warp >> 2, trow = (warp & 3) * 32 + lane;  // row of the tile = lane of tensor memory
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t t_s = tmem + lanes + kColS + tile * 128, t_o = tmem + lanes + kColO + tile * 128;
+        uint8_t* sq = smem + kOffQ + tile * kTileBytes;
+        const bool formed = a.softcap > 0.0f || a.slopes;
+        uint32_t n_s = 0, n_o = 0;  // S and O completions waited for
+        for (long long cur = run0; cur < run1 && walk_to(a, w, cur, n_groups);) {
+            const long long unit1 = w.unit0 + w.u.n_stages, stop = min(run1, unit1);
+            const int n_st = (int)(stop - cur), st0 = w.u.stage0 + (int)(cur - w.unit0);
+            const int tiles = w.u.rows > 128 ? 2 : 1;
+            cur = stop;
+            if (tile >= tiles) continue;
+            // ---- this thread's row ----
+            const int r = tile * 128 + trow;
+            int token = -1, head = 0, seq = w.u.seq, pos = 0, first = 0, end = 0;
+            float sc = 0.0f, slope = 0.0f;
+            if (r < w.u.rows) {
+                const int ft = a.prefix_phase ? 0 : a.batch.q_start[seq];
+                const int fr = w.u.row0 + r;
+                token = ft + fr / a.group;
+                head = w.h * a.group + fr % a.group;
+                if ((unsigned)token >= (unsigned)a.batch.n_rows) token = -1;
+                if (token >= 0 && a.prefix_phase) {
+                    seq = find_seq_thread(a.batch, token);
+                    if (seq < 0) token = -1;
+                }
+            }
+            if (token >= 0) {
+                const RowView v = row_view(a, seq, token);
+                pos = v.pos - shift;
+                first = max(v.first - shift, 0);
+                end = min(v.end - shift, w.u.n_keys);
+                if (a.slopes) slope = a.slopes[head];
+            }
+            {
+                // Q: fp16 as it is; bf16 with the row's power of two taken out
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q.p) + (long long)max(token, 0) * a.q.row +
+                                                                  (long long)head * a.q.head);
+                float up = 1.0f;
+                uint32_t top = 0;
+                if (a.q_dtype == kDtBF16 && token >= 0) {
+#pragma unroll 4
+                    for (int c = 0; c < 16; ++c) {
+                        const uint4 v = src[c];
+                        // the larger magnitude of two bf16, compared as integers
+                        top = max(top, max(max(v.x & 0x7fffu, (v.x >> 16) & 0x7fffu), max(v.y & 0x7fffu, (v.y >> 16) & 0x7fffu)));
+                        top = max(top, max(max(v.z & 0x7fffu, (v.z >> 16) & 0x7fffu), max(v.w & 0x7fffu, (v.w >> 16) & 0x7fffu)));
+                    }
+                }
+                const uint32_t ex = top >> 7;
+                const bool plain = ex < 2 || ex > 252;  // zero, subnormal and non-finite rows
+                const float down = plain ? 1.0f : __uint_as_float((254u - ex) << 23);
+                if (!plain) up = __uint_as_float(ex << 23);
+#pragma unroll 4
+                for (int c = 0; c < 16; ++c) {
+                    uint4 v = token >= 0 ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+                    if (a.q_dtype == kDtBF16) {
+                        uint32_t* x = &v.x;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            x[i] = h2u(__floats2half2_rn(__uint_as_float(x[i] << 16) * down, __uint_as_float(x[i] & 0xffff0000u) * down));
+                    }
+                    st_chunk(sq, trow, c, v);
+                }
+                sc = (formed ? a.scale : a.scale * 1.4426950408889634f) * up;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive(&q_full[tile]);
+            // page numbers outside the pool: the piece comes out as NaN
+            bool bad_page = false;
+            {
+                const int* table = a.prefix_phase ? a.prefix_table : a.batch.table + (size_t)w.u.seq * a.batch.table_stride;
+                const int n_table = a.prefix_phase ? (a.prefix_len + kPageTokens - 1) / kPageTokens : a.batch.table_stride;
+                for (int j = (st0 >> 1) + lane; 2 * j < st0 + n_st && j * kPageTokens < w.u.n_keys; j += 32)
+                    bad_page |= j >= n_table || (unsigned)table[j] >= (unsigned)a.pool.n_pages;
+                bad_page = __any_sync(0xffffffffu, bad_page);
+            }
+
+            float ref = token >= 0 ? -CUDART_INF_F : 0.0f, l = 0.0f;
+            // keys that every row of this warp sees
+            const int all_from = __reduce_max_sync(0xffffffffu, token >= 0 ? first : 0);
+            const int all_to = __reduce_min_sync(0xffffffffu, token >= 0 ? end : INT_MAX);
+            for (int i = 0; i < n_st; ++i) {
+                const int key0 = (st0 + i) * kStageKeys;
+                wait(&s_full[tile], n_s & 1);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                ++n_s;
+                tc_fence_after();
+                const bool masked = key0 < all_from || key0 + kStageKeys > all_to;  // uniform
+                const bool sees = max(first, key0) < min(end, key0 + kStageKeys);
+                if (formed) {
+                    // caps and distances: the scores are formed in place first, 32 columns at a
+                    // time (a rolled loop: unrolled over a row it outgrows the instruction cache)
+#pragma unroll 1
+                    for (int c0 = 0; c0 < kStageKeys; c0 += 32) {
+                        float s[32];
+                        tmem_ld32(t_s + c0, s);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) s[c] = score_log2(a, s[c] * sc, slope, pos, key0 + c0 + c);
+                        tmem_st32(t_s + c0, s);
+                    }
+                }
+                // scores of 64 columns in the log2 domain, from tensor memory
+                auto load_scores = [&](int half, float (&s)[64]) {
+                    tmem_ld64(t_s + 64 * half, s);
+                    if (masked) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) {
+                            const int key = key0 + 64 * half + c;
+                            if (key < first || key >= end) s[c] = -CUDART_INF_F;
+                        }
+                    }
+                };
+                const float2 mul = formed ? make_float2(1.0f, 1.0f) : make_float2(sc, sc);
+                uint32_t p[64];
+                float sum = 0.0f;
+                auto weights = [&]() {
+                    const float mu = ref == -CUDART_INF_F ? 0.0f : -ref;
+                    float2 s0 = make_float2(0.0f, 0.0f), s1 = make_float2(0.0f, 0.0f);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        float s[64];
+                        load_scores(half, s);
+#pragma unroll
+                        for (int c = 0; c < 64; c += 4) {
+                            float2 x = fma2(make_float2(s[c], s[c + 1]), mul, make_float2(mu, mu));
+                            float2 y = fma2(make_float2(s[c + 2], s[c + 3]), mul, make_float2(mu, mu));
+                            x = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+                            y = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+                            s0 = add2(s0, x);
+                            s1 = add2(s1, y);
+                            p[32 * half + c / 2] = h2u(__floats2half2_rn(x.x, x.y));
+                            p[32 * half + c / 2 + 1] = h2u(__floats2half2_rn(y.x, y.y));
+                        }
+                    }
+                    s0 = add2(s0, s1);
+                    sum = s0.x + s0.y;
+                };
+#pragma unroll 1
+                for (int round = 0;; ++round) {
+                    weights();
+                    const bool low = token >= 0 && (!(sum <= kSumMost) || (ref == -CUDART_INF_F && sees));
+                    if (round || !__any_sync(0xffffffffu, low)) break;
+                    // new references, 4 below the maximum; O follows
+                    float top = -CUDART_INF_F;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        float s[64];
+                        load_scores(half, s);
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) top = fmaxf(top, s[c] * mul.x);
+                    }
+                    const float now = low ? fmaxf(ref, top - 4.0f) : ref;
+                    const float f = now == ref ? 1.0f : exp2_fast(ref - now);
+                    ref = now;
+                    l *= f;
+                    if (i > 0) {  // the product before this S is complete, and none is in flight for this tile
+#pragma unroll 1
+                        for (int c = 0; c < 128; c += 32) {
+                            float o[32];
+                            tmem_ld32(t_o + c, o);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] *= f;
+                            tmem_st32(t_o + c, o);
+                        }
+                    }
+                }
+                l += sum;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    float x[32];
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(p[32 * half + c]);
+                    tmem_st32(t_s + 32 * half, x);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(&p_full[tile]);
+            }
+            wait(&o_full[tile], n_o & 1);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            ++n_o;
+            tc_fence_after();
+
+            // ---- the piece's end: O through shared memory (this warp's rows of Q), 64
+            // dims at a time, so that rows move as whole lines ----
+            const bool whole = w.unit0 >= run0 && unit1 <= run1;
+            const bool bad = bad_page || (!a.prefix_phase && end > (long long)a.batch.table_stride * kPageTokens);
+            if (bad) l = CUDART_NAN_F;
+            const int slot = w.unit0 < run0 ? 0 : 1;
+            const size_t at = (size_t)max(token, 0) * a.n_qh + head;
+            float M = ref, L = l, wo = 1.0f, wp = 0.0f;  // own and prefix weights
+            const bool final_rows = whole && !a.prefix_phase;
+            if (final_rows) {
+                if (a.prefix_len > 0 && token >= 0) {
+                    const float2 ml = a.prior_ml[at];
+                    M = fmaxf(ref, ml.x);
+                    wo = ref == M ? 1.0f : exp2_fast(ref - M);
+                    wp = ml.x == M ? 1.0f : exp2_fast(ml.x - M);
+                    L = l * wo + ml.y * wp;
+                }
+                const float inv = L != 0.0f ? 1.0f / L : 0.0f;
+                wo *= inv;
+                wp *= inv;
+                if (token >= 0 && a.lse) a.lse[at] = L == 0.0f ? -CUDART_INF_F : (M + log2f(L)) * 0.69314718055994531f;
+            } else if (token >= 0) {
+                if (whole) a.prior_ml[at] = make_float2(M, L);
+                else {
+                    float* rec = a.records + ((size_t)(blockIdx.x * 2 + slot) * kWideRows + r) * kRecordFloats;
+                    *reinterpret_cast<float2*>(rec + 128) = make_float2(M, L);
+                }
+            }
+            const bool finite = L * 0.0f == 0.0f;
+            uint32_t redo = 0;  // rows of this warp that an unseen value spoiled
+            // staging: 32 rows x 256 bytes in the warp's two 4 KB parts, 16-byte chunks turned by the row
+            auto stage = [&](int row, int chunk) {
+                return reinterpret_cast<float4*>(sq + (row >> 4) * 16384 + (warp & 3) * 4096 + (row & 15) * 256 + ((chunk ^ (row & 15)) << 4));
+            };
+#pragma unroll 1
+            for (int hf = 0; hf < 2; ++hf) {
+                float o[64];
+                tmem_ld64(t_o + 64 * hf, o);
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 16; ++c) *stage(lane, c) = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                __syncwarp();
+#pragma unroll 2
+                for (int it = 0; it < 16; ++it) {
+                    const int row = 2 * it + (lane >> 4), c = lane & 15;
+                    float4 v = *stage(row, c);
+                    const int tk = __shfl_sync(0xffffffffu, token, row), hd = __shfl_sync(0xffffffffu, head, row);
+                    const float fo = __shfl_sync(0xffffffffu, wo, row), fp = __shfl_sync(0xffffffffu, wp, row);
+                    const float LL = __shfl_sync(0xffffffffu, L, row);
+                    const bool fin = __shfl_sync(0xffffffffu, (int)finite, row) != 0;
+                    const size_t ra = (size_t)max(tk, 0) * a.n_qh + hd;
+                    const int d = 64 * hf + 4 * c;
+                    bool spoiled = false;
+                    if (tk >= 0) {
+                        if (final_rows) {
+                            float4 pv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            if (a.prefix_len > 0) pv = *reinterpret_cast<const float4*>(a.prior_acc + ra * kHeadDim + d);
+                            v.x = v.x * fo + pv.x * fp;
+                            v.y = v.y * fo + pv.y * fp;
+                            v.z = v.z * fo + pv.z * fp;
+                            v.w = v.w * fo + pv.w * fp;
+                            spoiled = fin && !((v.x + v.y + v.z + v.w) * 0.0f == 0.0f);
+                            if (LL == 0.0f) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            store_out4(a, tk, hd, d, v);
+                        } else if (whole) {
+                            *reinterpret_cast<float4*>(a.prior_acc + ra * kHeadDim + d) = v;
+                        } else {
+                            const int rr = tile * 128 + (warp & 3) * 32 + row;
+                            *reinterpret_cast<float4*>(a.records + ((size_t)(blockIdx.x * 2 + slot) * kWideRows + rr) * kRecordFloats + d) = v;
+                        }
+                    }
+                    const uint32_t votes = __ballot_sync(0xffffffffu, spoiled && LL != 0.0f);
+                    if (votes & 0xffffu) redo |= 1u << (2 * it);
+                    if (votes >> 16) redo |= 2u << (2 * it);
+                }
+            }
+            for (; redo; redo &= redo - 1) {
+                const int row = __ffs(redo) - 1;
+                const int tk = __shfl_sync(0xffffffffu, token, row), hd = __shfl_sync(0xffffffffu, head, row);
+                const int sq_ = __shfl_sync(0xffffffffu, seq, row);
+                store_out4(a, tk, hd, 4 * lane, slow_row<VT, KT>(a, sq_, tk, hd));
+            }
+            if (bad && lane == 0 && a.batch.status) atomicOr(a.batch.status, kErrBadPage);
+            __syncwarp();
+        }
+    } else if (warp < kMmaWarp) {
+        // ============================ producers ============================
+        // The codes of the next stage are loaded into registers as soon as this
+        // stage's are converted, so the loads run under the other operand's
+        // conversion and the waits.  Lanes are laid out so that the eight lanes of a
+        // 16-byte store phase hit distinct banks of the swizzled tiles:
+        //   128-byte rows, 4 a load: lane bits (chunk 0, 1), row 0, chunk 2, row 1;
+        //   64-byte rows, 8 a load:  lane bits block 0, (row 0, 1), block 1, row 2.
+        const int pw = warp - kSoftWarps;
+        const int ch = (lane & 3) + 4 * ((lane >> 3) & 1), rl = ((lane >> 2) & 1) + 2 * (lane >> 4);
+        const int bv = (lane & 1) + 2 * ((lane >> 3) & 1), rv = ((lane >> 1) & 3) + 4 * (lane >> 4);
+        constexpr int kMineK = KT == kKF16 ? 1 : kMine128;
+        constexpr int kMineV = VT == kVF16 ? 1 : (VT == kVQ8_0 ? kMine128 : kMine64);
+        uint4 kc[kMineK], vc[kMineV];
+        __half kd[kMineK], vd[kMineV], vm[kMineV];
+        uint32_t vh[kMineV];
+        uint32_t n_k = 0, n_v = 0;  // stages written
+        // the stage after (piece, stage): pieces follow each other without a break
+        struct Next {
+            const uint8_t* ph;
+            int hp, t0, valid;
+            bool there;
+        };
+        long long cur = run0, stop = run0;
+        int st = 0;
+        int pages = 0, pages_at = -1;
+        const int* table = nullptr;
+        int n_table = 0;
+        auto advance = [&]() -> Next {
+            Next x{nullptr, 0, 0, 0, false};
+            if (cur >= stop) {  // the next piece
+                if (cur >= run1 || !walk_to(a, w, cur, n_groups)) return x;
+                stop = min(run1, w.unit0 + w.u.n_stages);
+                st = w.u.stage0 + (int)(cur - w.unit0);
+                table = a.prefix_phase ? a.prefix_table : a.batch.table + (size_t)w.u.seq * a.batch.table_stride;
+                n_table = a.prefix_phase ? (a.prefix_len + kPageTokens - 1) / kPageTokens : a.batch.table_stride;
+                pages_at = -1;
+            }
+            const int j = st >> 1;
+            if (pages_at < 0 || j >= pages_at + 32) {
+                pages_at = j;
+                pages = j + lane < n_table ? table[j + lane] : -1;
+            }
+            int page = __shfl_sync(0xffffffffu, pages, j - pages_at);
+            if ((unsigned)page >= (unsigned)a.pool.n_pages) page = 0;  // some page: the softmax warps see it too
+            x.hp = page * n_kv + w.h;
+            x.ph = a.pool.pages + (size_t)x.hp * PG::kHeadBytes;
+            x.t0 = (st & 1) * kStageKeys;
+            x.valid = w.u.n_keys - st * kStageKeys;  // tokens of the stage that exist
+            x.there = true;
+            ++st;
+            ++cur;
+            return x;
+        };
+        auto load_k = [&](const Next& x) {
+            if constexpr (KT == kKQ8_0) {
+#pragma unroll
+                for (int g = 0; g < kMineK; ++g) {
+                    const int row = x.t0 + 4 * (pw + kProdWarps * g) + rl;
+                    if (pw + kProdWarps * g < 32) {
+                        kc[g] = *reinterpret_cast<const uint4*>(x.ph + row * 128 + 16 * ch);
+                        kd[g] = *reinterpret_cast<const __half*>(x.ph + PG::kOffKd + row * 8 + (ch & ~1));
+                    }
+                }
+            }
+        };
+        auto load_v = [&](const Next& x) {
+            const uint8_t* vq = x.ph + PG::kOffVq;
+            if constexpr (VT == kVQ8_0) {
+#pragma unroll
+                for (int g = 0; g < kMineV; ++g) {
+                    const int row = x.t0 + 4 * (pw + kProdWarps * g) + rl;
+                    if (pw + kProdWarps * g < 32) {
+                        vc[g] = *reinterpret_cast<const uint4*>(vq + row * 128 + 16 * ch);
+                        vd[g] = *reinterpret_cast<const __half*>(x.ph + PG::kOffVd + row * 8 + (ch & ~1));
+                    }
+                }
+            } else if constexpr (VT != kVF16) {
+#pragma unroll
+                for (int g = 0; g < kMineV; ++g) {
+                    const int row = x.t0 + 8 * (pw + kProdWarps * g) + rv;
+                    if (pw + kProdWarps * g < 16) {
+                        vc[g] = *reinterpret_cast<const uint4*>(vq + row * 64 + 16 * bv);
+                        vd[g] = *reinterpret_cast<const __half*>(x.ph + PG::kOffVd + row * 8 + 2 * bv);
+                        if constexpr (v_has_fifth(VT)) vh[g] = *reinterpret_cast<const uint32_t*>(x.ph + PG::kOffVh + row * 16 + 4 * bv);
+                        if constexpr (v_has_min(VT)) vm[g] = *reinterpret_cast<const __half*>(x.ph + PG::kOffVm + row * 8 + 2 * bv);
+                    }
+                }
+            }
+        };
+        Next x{nullptr, 0, 0, 0, false};
+        if (ok) x = advance();
+        if (x.there) {
+            load_k(x);
+            load_v(x);
+        }
+        while (x.there) {
+            const Next y = advance();
+            const int kb = n_k & 1, vb = n_v & 1;
+            // ---- K ----
+            if (n_k >= 2) {
+                wait(&k_free[kb], ((n_k >> 1) - 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) break;
+            }
+            uint8_t* kt = smem + kOffK + kb * kTileBytes;
+            if constexpr (KT == kKQ8_0) {
+#pragma unroll
+                for (int g = 0; g < kMineK; ++g) {
+                    const int row = 4 * (pw + kProdWarps * g) + rl;
+                    if (pw + kProdWarps * g < 32) {
+                        uint4 lo, hi;
+                        conv_s8(kc[g], h2u(__half2half2(kd[g])), lo, hi);
+                        st_chunk(kt, row, 2 * ch, lo);
+                        st_chunk(kt, row, 2 * ch + 1, hi);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive(&k_full[kb]);
+                if (y.there) load_k(y);  // behind the fence, which waits for loads in flight
+            } else if (pw == 0 && lane == 0) {
+                mbar_expect_tx(&k_full[kb], kTileBytes);
+                tma4(kt, &maps.k, 0, 0, x.t0, x.hp, &k_full[kb]);
+                tma4(kt + 16384, &maps.k, 0, 1, x.t0, x.hp, &k_full[kb]);
+            }
+            ++n_k;
+            // ---- V: rows that do not exist hold anything, their values become 0 ----
+            if (n_v >= 2) {
+                wait(&v_free[vb], ((n_v >> 1) - 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) break;
+            }
+            uint8_t* vt = smem + kOffV + vb * kTileBytes;
+            const __half zero = __float2half(0.0f);
+            if constexpr (VT == kVQ8_0) {
+#pragma unroll
+                for (int g = 0; g < kMineV; ++g) {
+                    const int row = 4 * (pw + kProdWarps * g) + rl;
+                    if (pw + kProdWarps * g < 32) {
+                        uint4 lo, hi;
+                        conv_s8(vc[g], h2u(__half2half2(row < x.valid ? vd[g] : zero)), lo, hi);
+                        st_chunk(vt, row, 2 * ch, lo);
+                        st_chunk(vt, row, 2 * ch + 1, hi);
+                    }
+                }
+            } else if constexpr (VT == kVF16) {
+                if (pw == 0 && lane == 0) {
+                    mbar_expect_tx(&v_raw[vb], kTileBytes);
+                    tma4(vt, &maps.v, 0, 0, PG::kOffVq / 256 + x.t0, x.hp, &v_raw[vb]);
+                    tma4(vt + 16384, &maps.v, 0, 1, PG::kOffVq / 256 + x.t0, x.hp, &v_raw[vb]);
+                }
+                wait(&v_raw[vb], (n_v >> 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                for (int c = pw * 32 + lane; x.valid < kStageKeys && c < 128 * 16; c += kProdWarps * 32)
+                    if ((c >> 4) >= x.valid) st_chunk(vt, c >> 4, c & 15, make_uint4(0u, 0u, 0u, 0u));
+            } else {
+#pragma unroll
+                for (int g = 0; g < kMineV; ++g) {
+                    const int row = 8 * (pw + kProdWarps * g) + rv;
+                    if (pw + kProdWarps * g < 16) {
+                        const bool there = row < x.valid;
+                        const __half2 d = __half2half2(there ? vd[g] : zero);
+                        const __half2 m = v_has_min(VT) ? __half2half2(there ? vm[g] : zero) : __float2half2_rn(0.0f);
+                        constexpr float kZero = v_has_min(VT) ? 0.0f : (VT == kVQ5_0 ? 16.0f : 8.0f);
+                        const __half2 z = __float2half2_rn(1024.0f + kZero);
+                        const uint32_t words[4] = {vc[g].x, vc[g].y, vc[g].z, vc[g].w};
+                        uint32_t o[2][8];  // dims 0..15 (low nibbles), 16..31 (high), as pairs
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int n = 0; n < 2; ++n) {
+                                const uint32_t c4 = (n ? words[k] >> 4 : words[k]) & 0x0f0f0f0fu;
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    uint32_t q2 = __byte_perm(c4, 0x64646464u, e ? 0x4342 : 0x4140);
+                                    if constexpr (v_has_fifth(VT)) {
+                                        const int bit = 16 * n + 4 * k + 2 * e;
+                                        q2 |= ((vh[g] >> bit) & 1u) << 4 | ((vh[g] >> (bit + 1)) & 1u) << 20;
+                                    }
+                                    const __half2 q = __hsub2(u2h(q2), z);
+                                    o[n][2 * k + e] = h2u(v_has_min(VT) ? __hfma2(q, d, m) : __hmul2(q, d));
+                                }
+                            }
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            st_chunk(vt, row, 4 * bv + c, make_uint4(o[c >> 1][4 * (c & 1)], o[c >> 1][4 * (c & 1) + 1],
+                                                                     o[c >> 1][4 * (c & 1) + 2], o[c >> 1][4 * (c & 1) + 3]));
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive(&v_full[vb]);
+            if (y.there) load_v(y);
+            ++n_v;
+            x = y;
+        }
+    } else {
+        if (lane == 0) {
+        // ============================ products ============================
+        uint32_t n_k = 0, n_v = 0, n_p[2] = {0, 0}, n_q[2] = {0, 0};
+        for (long long cur = run0; ok && cur < run1 && walk_to(a, w, cur, n_groups);) {
+            const long long stop = min(run1, w.unit0 + w.u.n_stages);
+            const int n_st = (int)(stop - cur);
+            const int tiles = w.u.rows > 128 ? 2 : 1;
+            cur = stop;
+            auto scores = [&](int t, int kb) {
+                const uint32_t q = smem_u32(smem + kOffQ + t * kTileBytes), k = smem_u32(smem + kOffK + kb * kTileBytes);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) tc_mma_f16(tmem + kColS + 128 * t, desc_k(q, kk), desc_k(k, kk), kIdescS, kk > 0);
+                tc_commit(&s_full[t]);
+            };
+            if (!wait(&k_full[n_k & 1], (n_k >> 1) & 1)) break;
+            for (int t = 0; t < tiles && wait(&q_full[t], n_q[t] & 1); ++t) {
+                ++n_q[t];
+                tc_fence_after();
+                scores(t, n_k & 1);
+            }
+            if (!ok) break;
+            tc_commit(&k_free[n_k & 1]);
+            ++n_k;
+            for (int i = 0; i < n_st && ok; ++i) {
+                const int vb = n_v & 1;
+                if (!wait(&v_full[vb], (n_v >> 1) & 1)) break;
+                for (int t = 0; t < tiles; ++t) {
+                    if (!wait(&p_full[t], n_p[t] & 1)) break;
+                    ++n_p[t];
+                    tc_fence_after();
+                    const uint32_t v = smem_u32(smem + kOffV + vb * kTileBytes);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * kk, desc_mn(v, kk), kIdescPV, i > 0 || kk > 0);
+                    if (t == tiles - 1) tc_commit(&v_free[vb]);
+                    if (i + 1 < n_st) {
+                        if (t == 0 && !wait(&k_full[n_k & 1], (n_k >> 1) & 1)) break;
+                        tc_fence_after();
+                        scores(t, n_k & 1);
+                        if (t == tiles - 1) {
+                            tc_commit(&k_free[n_k & 1]);
+                            ++n_k;
+                        }
+                    } else {
+                        tc_commit(&o_full[t]);
+                    }
+                }
+                ++n_v;
+            }
+        }
+        if (run0 < run1) {  // nothing is in flight when the memory is given back
+            tc_commit(done);
+            mbar_wait_bounded(done, 0, a.batch.status);
+        }
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---- the join of units that several CTAs share: block (CTA border, rows); the
+// border that is the first inside its unit does it, a warp a row ----
+constexpr int kJoinWarps = 8;
+template <int VT, int KT>
+__global__ void __launch_bounds__(kJoinWarps * 32) wide_join_kernel(const __grid_constant__ AttendPagesArgs a, int n_ctas) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n_groups = a.plan->n_groups;
+    const long long total = a.plan->total * a.pool.n_kv, per = max(1ll, (total + n_ctas - 1) / n_ctas);
+    const long long x = per * (blockIdx.x + 1);  // the border before CTA blockIdx.x + 1
+    if (x >= total) return;
+    Walk w;
+    w.group = find_group(a, x, n_groups);
+    w.u = a.units[w.group];
+    if (!walk_to(a, w, x, n_groups) || w.unit0 == x || w.unit0 < x - per) return;  // between units, or not the first border
+    const long long unit1 = w.unit0 + w.u.n_stages;
+    const int c0 = blockIdx.x, c1 = (int)((unit1 - 1) / per);
+    const int ft = a.prefix_phase ? 0 : a.batch.q_start[w.u.seq];
+    for (int r = blockIdx.y * kJoinWarps + warp; r < w.u.rows; r += gridDim.y * kJoinWarps) {
+        const int fr = w.u.row0 + r, token = ft + fr / a.group, head = w.h * a.group + fr % a.group;
+        if ((unsigned)token >= (unsigned)a.batch.n_rows || (a.prefix_phase && find_seq_thread(a.batch, token) < 0)) continue;
+        auto record = [&](int c) { return a.records + ((size_t)(c * 2 + (c == c0 ? 1 : 0)) * kWideRows + r) * kRecordFloats; };
+        float M = -CUDART_INF_F, L = 0.0f;
+        for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, record(c)[128]);
+#pragma unroll
+        for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int c = c0; c <= c1; ++c) {
+            const float4 v = reinterpret_cast<const float4*>(record(c))[lane];
+            const float2 ml = *reinterpret_cast<const float2*>(record(c) + 128);
+            const float f = ml.x == M ? 1.0f : exp2_fast(ml.x - M);
+            acc.x = fmaf(v.x, f, acc.x);
+            acc.y = fmaf(v.y, f, acc.y);
+            acc.z = fmaf(v.z, f, acc.z);
+            acc.w = fmaf(v.w, f, acc.w);
+            L = fmaf(ml.y, f, L);
+        }
+        finish_row<VT, KT>(a, w.u.seq, token, head, acc, M, L);
+    }
+}
+
+template <int VT, int KT>
+cudaError_t launch(const AttendPagesArgs& a, const PageMaps& maps, int n_sms, cudaStream_t s) {
+    static std::atomic<unsigned long long> configured{0};  // the shared-memory opt-in is per device
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 64 || !(configured.load(std::memory_order_acquire) & (1ull << dev))) {
+        const cudaError_t e = cudaFuncSetAttribute(attend_wide_kernel<VT, KT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) configured.fetch_or(1ull << dev, std::memory_order_acq_rel);
+    }
+    const int ctas = std::min(kWideCtas, n_sms);
+    const long long groups = wide_groups(a.batch.n_rows, a.group, a.prefix_phase ? 1 : a.batch.n_seqs);
+    wide_plan_kernel<<<1, kPlanThreads, 0, s>>>(a, (int)std::min(groups, 0x7fffffffll));
+    attend_wide_kernel<VT, KT><<<ctas, kThreads, kSmem, s>>>(a, maps);
+    if (ctas > 1) wide_join_kernel<VT, KT><<<dim3(ctas - 1, 8), kJoinWarps * 32, 0, s>>>(a, ctas);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attend_wide(const AttendPagesArgs& a, const PageMaps& maps, int n_sms, cudaStream_t s) {
+    if (a.pool.k_type == kKF16) return launch<kVF16, kKF16>(a, maps, n_sms, s);
+    switch (a.pool.v_type) {
+        case kVF16: return launch<kVF16, kKQ8_0>(a, maps, n_sms, s);
+        case kVQ4_1: return launch<kVQ4_1, kKQ8_0>(a, maps, n_sms, s);
+        case kVQ5_0: return launch<kVQ5_0, kKQ8_0>(a, maps, n_sms, s);
+        case kVQ5_1: return launch<kVQ5_1, kKQ8_0>(a, maps, n_sms, s);
+        case kVQ8_0: return launch<kVQ8_0, kKQ8_0>(a, maps, n_sms, s);
+        default: return launch<kVQ4_0, kKQ8_0>(a, maps, n_sms, s);
+    }
+}
+
+}  // namespace kvs
