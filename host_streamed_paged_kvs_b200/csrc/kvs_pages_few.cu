@@ -57,8 +57,6 @@ constexpr int kStageKeys = 128;
 constexpr int kQRow = 288;                         // bytes of a Q row in shared memory: 32 mod 128, so that 4 rows x 32 B are distinct banks
 constexpr int kRedRow = 132;                       // floats of a row in the join buffer
 constexpr int kRedBytes = kConsumers * 8 * kRedRow * 4;
-// Waits are bounded; the bound leaves room for rows recomputed the slow way.
-constexpr uint64_t kWaitNs = 10000000000ull;
 
 // A piece: rows of one unit and the stages of it that this CTA takes.
 template <int ROWS>
@@ -286,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                 if (seq < n_seqs) s = seq_of<ROWS>(a, seq);
             }
             Piece<ROWS>& p = pieces[n_pieces & 1];
-            if (n_pieces >= 2) ok = mbar_wait_bounded(&p_empty[n_pieces & 1], ((n_pieces >> 1) - 1) & 1, a.batch.status, kWaitNs);
+            if (n_pieces >= 2) ok = wait_phase(&p_empty[n_pieces & 1], ((n_pieces >> 1) - 1) & 1, a.batch.status);
             if (!ok || cur >= run1 || seq >= n_seqs) {
                 if (lane == 0) p.n_stages = -1;
                 __syncwarp();
@@ -401,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                 int page = __shfl_sync(0xffffffffu, pages, j - pages_at);
                 const int buf = issued % kStages;
                 if (issued >= kStages &&
-                    !mbar_wait_bounded(&empty[buf], ((issued / kStages) - 1) & 1, a.batch.status, kWaitNs)) {
+                    !wait_phase(&empty[buf], ((issued / kStages) - 1) & 1, a.batch.status)) {
                     ok = false;
                     break;
                 }
@@ -442,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
         }
         // a wait gave up: the copies in flight land before the memory is given back
         for (int k = max(0, issued - kStages); !ok && k < issued; ++k)
-            mbar_wait_bounded(&full[k % kStages], (k / kStages) & 1, a.batch.status);
+            wait_phase(&full[k % kStages], (k / kStages) & 1, a.batch.status);
         return;
     }
 
@@ -456,13 +454,13 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
     auto consumers_sync = [&]() -> bool {
         __syncwarp();
         if (lane == 0) arrive(c_bar);
-        const bool ok = mbar_wait_bounded(c_bar, c_phase, a.batch.status, kWaitNs);
+        const bool ok = wait_phase(c_bar, c_phase, a.batch.status);
         c_phase ^= 1;
         return __all_sync(0xffffffffu, ok);
     };
     for (int n = 0;; ++n) {
         Piece<ROWS>& p = pieces[n & 1];
-        if (!mbar_wait_bounded(&p_full[n & 1], (n >> 1) & 1, a.batch.status, kWaitNs)) return;
+        if (!wait_phase(&p_full[n & 1], (n >> 1) & 1, a.batch.status)) return;
         if (p.n_stages < 0) return;
         float o[8][NT][4];
         float ref[NT][2], l[NT][2], sc[NT][2];
@@ -483,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
         bool ok = true;
         for (int i = 0; i < p.n_stages; ++i, ++used) {
             const int buf = used % kStages;
-            ok = mbar_wait_bounded(&full[buf], (used / kStages) & 1, a.batch.status, kWaitNs);
+            ok = wait_phase(&full[buf], (used / kStages) & 1, a.batch.status);
             if (!__all_sync(0xffffffffu, ok)) return;
             const uint8_t* sb = smem + buf * G::kBytes;
             const int key0 = (p.first_stage + i) * kStageKeys;  // the stage's first key

@@ -7,8 +7,28 @@
 #include <math_constants.h>
 
 #include "kvs_pages.h"
+#include "kvs_ptx.cuh"
 
 namespace kvs {
+
+// Waits for an mbarrier phase, for at most about 10 s (rows may be recomputed the
+// slow way meanwhile).  The clock is read only after many failed tries: reading
+// it costs more than the wait for a barrier that is nearly always complete.
+constexpr uint64_t kPagesWaitNs = 10000000000ull;
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int* err) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 0;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 1023) == 1023) {
+            const uint64_t t = globaltimer_ns();
+            if (t0 == 0) t0 = t;
+            else if (t - t0 > kPagesWaitNs) {
+                if (err) atomicOr(err, kErrWaitTimeout);
+                return false;
+            }
+        }
+    }
+}
 
 // Value d of the K or V row of token t in a page head, fp32 (exact).
 template <int VT, int KT>

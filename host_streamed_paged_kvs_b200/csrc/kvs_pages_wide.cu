@@ -13,17 +13,19 @@
 // stages form one list and every CTA takes an equal run of it.  Units that
 // several CTAs share leave records, which a last launch joins in CTA order.
 //
-// Roles, handing work over by mbarriers only, 12 warps (3 a sub-partition, so
-// that each may have 168 registers):
+// Roles, handing work over by mbarriers only, 16 warps:
 //   warps 0..3, 4..7: softmax of tile 0 and 1, a thread a row.  S comes out of
-//     tensor memory 64 columns at a time; weights 2^(s - r) are formed with the
-//     row's kept reference, packed to fp16 and put back over S.  A row's maximum
-//     is taken only when its weights' sum says that the reference is too low
-//     (over 2^13, or the first keys seen): then the row of O is rescaled.
-//   warps 8..10: convert K and V of each stage to fp16 operand tiles (128-byte
-//     swizzle); the next stage's codes are in registers while they wait.
-//     fp16 rows come by TMA instead, as they are.
-//   warp 11: one thread issues S = Q K^T and O += P V of the two tiles in turn,
+//     tensor memory 16 columns at a time; the weights 2^(s - r) with the row's
+//     kept reference are packed to fp16 and put back over S.  A row's maximum is
+//     taken only when its weights' sum says that the reference is too low (over
+//     2^13, or the first keys seen): then the row of O is rescaled.
+//   warps 8..11 and 12..14: convert K and V of each stage to fp16 operand tiles
+//     (128-byte swizzle); the next stage's codes are on their way to registers
+//     meanwhile.  A warp converts one operand only: the fence that hands a tile to
+//     the tensor cores waits for the warp's loads in flight, so loads of the other
+//     operand would be waited for too (a 256-token chunk at 64K: 432 us).  fp16
+//     rows come by TMA instead, as they are.
+//   warp 15: one thread issues S = Q K^T and O += P V of the two tiles in turn,
 //     so that one tile's softmax runs under the other's products.
 // K and V are rounded to fp16 once (d q), the weights once; sums and softmax
 // statistics are fp32.
@@ -42,7 +44,7 @@
 namespace kvs {
 namespace {
 
-constexpr int kSoftWarps = 8, kProdWarps = 3, kMmaWarp = kSoftWarps + kProdWarps;
+constexpr int kSoftWarps = 8, kKWarps = 4, kVWarps = 3, kMmaWarp = kSoftWarps + kKWarps + kVWarps;
 constexpr int kThreads = (kMmaWarp + 1) * 32;
 constexpr int kStageKeys = 128;
 constexpr int kTileBytes = 128 * kHeadDim * 2;        // 32 KB: an operand of 128 rows x 128 fp16
@@ -53,7 +55,6 @@ constexpr int kOffV = kOffK + kBufs * kTileBytes;
 constexpr int kOffBar = kOffV + kBufs * kTileBytes;
 constexpr size_t kSmem = 1024 + kOffBar + 256;
 static_assert(kSmem <= 232448, "shared memory");
-constexpr uint64_t kWaitNs = 10000000000ull;          // leaves room for rows recomputed the slow way
 constexpr float kSumMost = 8192.0f;                   // a row's weights of one stage: fp16 holds each
 constexpr uint32_t kColS = 0, kColO = 256;            // tensor memory columns, + 128 per tile
 // f16 x f16 -> f32, M = N = 128, A K-major (Q) or from tensor memory (P); B K-major (K), MN-major (V)
@@ -88,10 +89,33 @@ __device__ __forceinline__ void tma4(void* dst, const CUtensorMap* map, int c0, 
         "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Products and commits by the elected lane of a converged warp (`one` is 1 in
+// that lane): descriptors stay warp-uniform values, so that an instruction is
+// issued in a few cycles.  Inside a one-lane branch each descriptor word is
+// moved to a uniform register first, 60 to 150 cycles an instruction beside the
+// other warps' arithmetic, which made the issue the kernel's bound.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t one) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t one) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void commit_one(uint64_t* bar, uint32_t one) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one;
 }
 __device__ __forceinline__ unsigned long long f2_bits(float a, float b) {
     return (unsigned long long)__float_as_uint(a) | ((unsigned long long)__float_as_uint(b) << 32);
@@ -107,6 +131,31 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a.x, a.y)), "l"(f2_bits(b.x, b.y)));
     return make_float2(__uint_as_float((uint32_t)r), __uint_as_float((uint32_t)(r >> 32)));
 }
+// 16 columns of tensor memory on their way into registers; tmem_here makes them usable
+__device__ __forceinline__ void tmem_fetch(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_here(uint32_t (&r)[16]) {
+    // the wait names the registers, so no use of them is scheduled ahead of it
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+// 16 columns into tensor memory, without waiting for them
+__device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void st_chunk(uint8_t* tile, int row, int c, uint4 v) {
     *reinterpret_cast<uint4*>(tile + chunk_off(row, c)) = v;
 }
@@ -254,8 +303,9 @@ __device__ __forceinline__ int find_group(const AttendPagesArgs& a, long long x,
     return lo;
 }
 
-// a producer warp's loads of a stage: 128-byte rows 4 a load, 64-byte rows 8 a load
-constexpr int kMine128 = (32 + kProdWarps - 1) / kProdWarps, kMine64 = (16 + kProdWarps - 1) / kProdWarps;
+// one of n_warps producer warps: its loads of a stage, 128-byte rows 4 a load, 64-byte rows 8 a load
+__host__ __device__ constexpr int mine128(int n_warps) { return (32 + n_warps - 1) / n_warps; }
+__host__ __device__ constexpr int mine64(int n_warps) { return (16 + n_warps - 1) / n_warps; }
 
 // 16 int8 codes times d as two 16-byte chunks
 __device__ __forceinline__ void conv_s8(const uint4& c, uint32_t d2, uint4& lo, uint4& hi) {
@@ -275,6 +325,7 @@ template <int VT, int KT>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_wide_kernel(const __grid_constant__ AttendPagesArgs a, const __grid_constant__ PageMaps maps) {
     using PG = PageGeom<VT, KT>;
+    constexpr bool kNibbles = VT != kVF16 && VT != kVQ8_0;  // O's columns: dims 0, 2, 1, 3 of every four
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
@@ -301,9 +352,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 32) {
         *sAbort = 0;
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&k_full[i], KT == kKF16 ? 1 : kProdWarps);
+            mbar_init(&k_full[i], KT == kKF16 ? 1 : kKWarps);
             mbar_init(&k_free[i], 1);
-            mbar_init(&v_full[i], kProdWarps);
+            mbar_init(&v_full[i], kVWarps);
             mbar_init(&v_free[i], 1);
             mbar_init(&v_raw[i], 1);
             mbar_init(&s_full[i], 1);
@@ -328,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = run0 < run1;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {  // by one thread or a whole warp
         if (!ok || *sAbort) return ok = false;
-        if (!mbar_wait_bounded(bar, parity, a.batch.status, kWaitNs)) {
+        if (!wait_phase(bar, parity, a.batch.status)) {
             ok = false;
             *sAbort = 1;
         }
@@ -392,7 +443,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const uint32_t ex = top >> 7;
                 const bool plain = ex < 2 || ex > 252;  // zero, subnormal and non-finite rows
-                const float down = plain ? 1.0f : __uint_as_float((254u - ex) << 23);
+                // a negative scale turns Q, so that the largest product is the largest score
+                const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
+                const float down = plain ? sign : sign * __uint_as_float((254u - ex) << 23);
                 if (!plain) up = __uint_as_float(ex << 23);
 #pragma unroll 4
                 for (int c = 0; c < 16; ++c) {
@@ -402,10 +455,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             x[i] = h2u(__floats2half2_rn(__uint_as_float(x[i] << 16) * down, __uint_as_float(x[i] & 0xffff0000u) * down));
+                    } else if (a.scale < 0.0f) {
+                        v = make_uint4(v.x ^ 0x80008000u, v.y ^ 0x80008000u, v.z ^ 0x80008000u, v.w ^ 0x80008000u);
                     }
                     st_chunk(sq, trow, c, v);
                 }
-                sc = (formed ? a.scale : a.scale * 1.4426950408889634f) * up;
+                sc = fabsf(formed ? a.scale : a.scale * 1.4426950408889634f) * up;
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -431,70 +486,70 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++n_s;
                 tc_fence_after();
                 const bool masked = key0 < all_from || key0 + kStageKeys > all_to;  // uniform
-                const bool sees = max(first, key0) < min(end, key0 + kStageKeys);
-                if (formed) {
-                    // caps and distances: the scores are formed in place first, 32 columns at a
-                    // time (a rolled loop: unrolled over a row it outgrows the instruction cache)
+                if (formed || masked) {
+                    // caps, distances and masks: the scores are formed in place first, so that
+                    // the two passes below stay short (unrolled code for every case outgrows the
+                    // instruction cache, which the other roles' loops share)
+#pragma unroll 1
+                    for (int c0 = 0; c0 < kStageKeys; c0 += 32) {
+                        float s[32];
+                        tmem_ld32(t_s + c0, s);
+                        if (formed) {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) s[c] = score_log2(a, s[c] * sc, slope, pos, key0 + c0 + c);
+                        }
+                        const int f = first - key0 - c0, e = end - key0 - c0;
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (c < f || c >= e) s[c] = -CUDART_INF_F;
+                        tmem_st32(t_s + c0, s);
+                    }
+                }
+                const float mul = formed ? 1.0f : sc;
+                // ---- weights with the row's kept reference, 16 columns at a time, the next
+                // ones on their way; put back over the scores when the row's sum says that
+                // the reference stands ----
+                const float2 mul2 = make_float2(mul, mul);
+                uint32_t p[64];
+                float sum;
+#pragma unroll 1
+                for (int round = 0;; ++round) {
+                    const float mu = ref == -CUDART_INF_F ? 0.0f : -ref;
+                    const float2 mu2 = make_float2(mu, mu);
+                    float2 s0 = make_float2(0.0f, 0.0f), s1 = make_float2(0.0f, 0.0f);
+                    uint32_t r[2][16];
+                    tmem_fetch(t_s, r[0]);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        uint32_t(&x)[16] = r[k & 1];
+                        tmem_here(x);
+                        if (k < 7) tmem_fetch(t_s + 16 * (k + 1), r[(k + 1) & 1]);
+#pragma unroll
+                        for (int c = 0; c < 16; c += 4) {
+                            float2 u = fma2(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), mul2, mu2);
+                            float2 v = fma2(make_float2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), mul2, mu2);
+                            u = make_float2(exp2_fast(u.x), exp2_fast(u.y));
+                            v = make_float2(exp2_fast(v.x), exp2_fast(v.y));
+                            s0 = add2(s0, u);
+                            s1 = add2(s1, v);
+                            p[8 * k + c / 2] = h2u(__floats2half2_rn(u.x, u.y));
+                            p[8 * k + c / 2 + 1] = h2u(__floats2half2_rn(v.x, v.y));
+                        }
+                    }
+                    s0 = add2(s0, s1);
+                    sum = s0.x + s0.y;
+                    const bool low = token >= 0 && (!(sum <= kSumMost) || (ref == -CUDART_INF_F && max(first, key0) < min(end, key0 + kStageKeys)));
+                    if (round || !__any_sync(0xffffffffu, low)) break;
+                    // the row's maximum: the reference goes 4 below it, and O with it
+                    float top = -CUDART_INF_F;
 #pragma unroll 1
                     for (int c0 = 0; c0 < kStageKeys; c0 += 32) {
                         float s[32];
                         tmem_ld32(t_s + c0, s);
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) s[c] = score_log2(a, s[c] * sc, slope, pos, key0 + c0 + c);
-                        tmem_st32(t_s + c0, s);
+                        for (int c = 0; c < 32; ++c) top = fmaxf(top, s[c]);
                     }
-                }
-                // scores of 64 columns in the log2 domain, from tensor memory
-                auto load_scores = [&](int half, float (&s)[64]) {
-                    tmem_ld64(t_s + 64 * half, s);
-                    if (masked) {
-#pragma unroll
-                        for (int c = 0; c < 64; ++c) {
-                            const int key = key0 + 64 * half + c;
-                            if (key < first || key >= end) s[c] = -CUDART_INF_F;
-                        }
-                    }
-                };
-                const float2 mul = formed ? make_float2(1.0f, 1.0f) : make_float2(sc, sc);
-                uint32_t p[64];
-                float sum = 0.0f;
-                auto weights = [&]() {
-                    const float mu = ref == -CUDART_INF_F ? 0.0f : -ref;
-                    float2 s0 = make_float2(0.0f, 0.0f), s1 = make_float2(0.0f, 0.0f);
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        float s[64];
-                        load_scores(half, s);
-#pragma unroll
-                        for (int c = 0; c < 64; c += 4) {
-                            float2 x = fma2(make_float2(s[c], s[c + 1]), mul, make_float2(mu, mu));
-                            float2 y = fma2(make_float2(s[c + 2], s[c + 3]), mul, make_float2(mu, mu));
-                            x = make_float2(exp2_fast(x.x), exp2_fast(x.y));
-                            y = make_float2(exp2_fast(y.x), exp2_fast(y.y));
-                            s0 = add2(s0, x);
-                            s1 = add2(s1, y);
-                            p[32 * half + c / 2] = h2u(__floats2half2_rn(x.x, x.y));
-                            p[32 * half + c / 2 + 1] = h2u(__floats2half2_rn(y.x, y.y));
-                        }
-                    }
-                    s0 = add2(s0, s1);
-                    sum = s0.x + s0.y;
-                };
-#pragma unroll 1
-                for (int round = 0;; ++round) {
-                    weights();
-                    const bool low = token >= 0 && (!(sum <= kSumMost) || (ref == -CUDART_INF_F && sees));
-                    if (round || !__any_sync(0xffffffffu, low)) break;
-                    // new references, 4 below the maximum; O follows
-                    float top = -CUDART_INF_F;
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        float s[64];
-                        load_scores(half, s);
-#pragma unroll
-                        for (int c = 0; c < 64; ++c) top = fmaxf(top, s[c] * mul.x);
-                    }
-                    const float now = low ? fmaxf(ref, top - 4.0f) : ref;
+                    const float now = low ? fmaxf(ref, top * mul - 4.0f) : ref;
                     const float f = now == ref ? 1.0f : exp2_fast(ref - now);
                     ref = now;
                     l *= f;
@@ -511,12 +566,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 l += sum;
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    float x[32];
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(p[32 * half + c]);
-                    tmem_st32(t_s + 32 * half, x);
-                }
+                for (int k = 0; k < 4; ++k) tmem_put16(t_s + 16 * k, p + 16 * k);
+                tmem_put_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive(&p_full[tile]);
@@ -566,7 +617,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld64(t_o + 64 * hf, o);
                 __syncwarp();
 #pragma unroll
-                for (int c = 0; c < 16; ++c) *stage(lane, c) = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                for (int c = 0; c < 16; ++c)
+                    *stage(lane, c) = kNibbles ? make_float4(o[4 * c], o[4 * c + 2], o[4 * c + 1], o[4 * c + 3])
+                                               : make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
                 __syncwarp();
 #pragma unroll 2
                 for (int it = 0; it < 16; ++it) {
@@ -614,20 +667,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < kMmaWarp) {
         // ============================ producers ============================
         // The codes of the next stage are loaded into registers as soon as this
-        // stage's are converted, so the loads run under the other operand's
-        // conversion and the waits.  Lanes are laid out so that the eight lanes of a
+        // stage's are converted.  Lanes are laid out so that the eight lanes of a
         // 16-byte store phase hit distinct banks of the swizzled tiles:
         //   128-byte rows, 4 a load: lane bits (chunk 0, 1), row 0, chunk 2, row 1;
         //   64-byte rows, 8 a load:  lane bits block 0, (row 0, 1), block 1, row 2.
-        const int pw = warp - kSoftWarps;
         const int ch = (lane & 3) + 4 * ((lane >> 3) & 1), rl = ((lane >> 2) & 1) + 2 * (lane >> 4);
         const int bv = (lane & 1) + 2 * ((lane >> 3) & 1), rv = ((lane >> 1) & 3) + 4 * (lane >> 4);
-        constexpr int kMineK = KT == kKF16 ? 1 : kMine128;
-        constexpr int kMineV = VT == kVF16 ? 1 : (VT == kVQ8_0 ? kMine128 : kMine64);
-        uint4 kc[kMineK], vc[kMineV];
-        __half kd[kMineK], vd[kMineV], vm[kMineV];
-        uint32_t vh[kMineV];
-        uint32_t n_k = 0, n_v = 0;  // stages written
         // the stage after (piece, stage): pieces follow each other without a break
         struct Next {
             const uint8_t* ph;
@@ -665,203 +710,223 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++cur;
             return x;
         };
-        auto load_k = [&](const Next& x) {
-            if constexpr (KT == kKQ8_0) {
-#pragma unroll
-                for (int g = 0; g < kMineK; ++g) {
-                    const int row = x.t0 + 4 * (pw + kProdWarps * g) + rl;
-                    if (pw + kProdWarps * g < 32) {
-                        kc[g] = *reinterpret_cast<const uint4*>(x.ph + row * 128 + 16 * ch);
-                        kd[g] = *reinterpret_cast<const __half*>(x.ph + PG::kOffKd + row * 8 + (ch & ~1));
-                    }
-                }
-            }
-        };
-        auto load_v = [&](const Next& x) {
-            const uint8_t* vq = x.ph + PG::kOffVq;
-            if constexpr (VT == kVQ8_0) {
-#pragma unroll
-                for (int g = 0; g < kMineV; ++g) {
-                    const int row = x.t0 + 4 * (pw + kProdWarps * g) + rl;
-                    if (pw + kProdWarps * g < 32) {
-                        vc[g] = *reinterpret_cast<const uint4*>(vq + row * 128 + 16 * ch);
-                        vd[g] = *reinterpret_cast<const __half*>(x.ph + PG::kOffVd + row * 8 + (ch & ~1));
-                    }
-                }
-            } else if constexpr (VT != kVF16) {
-#pragma unroll
-                for (int g = 0; g < kMineV; ++g) {
-                    const int row = x.t0 + 8 * (pw + kProdWarps * g) + rv;
-                    if (pw + kProdWarps * g < 16) {
-                        vc[g] = *reinterpret_cast<const uint4*>(vq + row * 64 + 16 * bv);
-                        vd[g] = *reinterpret_cast<const __half*>(x.ph + PG::kOffVd + row * 8 + 2 * bv);
-                        if constexpr (v_has_fifth(VT)) vh[g] = *reinterpret_cast<const uint32_t*>(x.ph + PG::kOffVh + row * 16 + 4 * bv);
-                        if constexpr (v_has_min(VT)) vm[g] = *reinterpret_cast<const __half*>(x.ph + PG::kOffVm + row * 8 + 2 * bv);
-                    }
-                }
-            }
-        };
-        Next x{nullptr, 0, 0, 0, false};
-        if (ok) x = advance();
-        if (x.there) {
-            load_k(x);
-            load_v(x);
-        }
-        while (x.there) {
-            const Next y = advance();
-            const int kb = n_k & 1, vb = n_v & 1;
+        if (warp < kSoftWarps + kKWarps) {
             // ---- K ----
-            if (n_k >= 2) {
-                wait(&k_free[kb], ((n_k >> 1) - 1) & 1);
-                if (!__all_sync(0xffffffffu, ok)) break;
-            }
-            uint8_t* kt = smem + kOffK + kb * kTileBytes;
-            if constexpr (KT == kKQ8_0) {
+            const int pw = warp - kSoftWarps;
+            constexpr int kMine = KT == kKF16 ? 1 : mine128(kKWarps);
+            uint4 kc[kMine];
+            __half kd[kMine];
+            auto load_k = [&](const Next& x) {
+                if constexpr (KT == kKQ8_0) {
 #pragma unroll
-                for (int g = 0; g < kMineK; ++g) {
-                    const int row = 4 * (pw + kProdWarps * g) + rl;
-                    if (pw + kProdWarps * g < 32) {
+                    for (int g = 0; g < kMine; ++g) {
+                        const int row = x.t0 + 4 * (pw + kKWarps * g) + rl;
+                        if (pw + kKWarps * g < 32) {
+                            kc[g] = *reinterpret_cast<const uint4*>(x.ph + row * 128 + 16 * ch);
+                            kd[g] = *reinterpret_cast<const __half*>(x.ph + PG::kOffKd + row * 8 + (ch & ~1));
+                        }
+                    }
+                }
+            };
+            Next x{nullptr, 0, 0, 0, false};
+            if (ok) x = advance();
+            if (x.there) load_k(x);
+            for (uint32_t n = 0; x.there; ++n) {
+                const Next y = advance();
+                const int kb = n & 1;
+                if (n >= 2) {
+                    wait(&k_free[kb], ((n >> 1) - 1) & 1);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                }
+                uint8_t* kt = smem + kOffK + kb * kTileBytes;
+                if constexpr (KT == kKQ8_0) {
+#pragma unroll
+                    for (int g = 0; g < kMine; ++g) {
+                        const int row = 4 * (pw + kKWarps * g) + rl;
                         uint4 lo, hi;
                         conv_s8(kc[g], h2u(__half2half2(kd[g])), lo, hi);
                         st_chunk(kt, row, 2 * ch, lo);
                         st_chunk(kt, row, 2 * ch + 1, hi);
                     }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) arrive(&k_full[kb]);
+                    if (y.there) load_k(y);
+                } else if (pw == 0 && lane == 0) {
+                    mbar_expect_tx(&k_full[kb], kTileBytes);
+                    tma4(kt, &maps.k, 0, 0, x.t0, x.hp, &k_full[kb]);
+                    tma4(kt + 16384, &maps.k, 0, 1, x.t0, x.hp, &k_full[kb]);
+                }
+                x = y;
+            }
+        } else {
+            // ---- V: rows that do not exist hold anything, their values become 0 ----
+            const int pw = warp - kSoftWarps - kKWarps;
+            constexpr int kMine = VT == kVF16 ? 1 : (VT == kVQ8_0 ? mine128(kVWarps) : mine64(kVWarps));
+            uint4 vc[kMine];
+            __half vd[kMine], vm[kMine];
+            uint32_t vh[kMine];
+            auto load_v = [&](const Next& x) {
+                const uint8_t* vq = x.ph + PG::kOffVq;
+                if constexpr (VT == kVQ8_0) {
+#pragma unroll
+                    for (int g = 0; g < kMine; ++g) {
+                        const int row = x.t0 + 4 * (pw + kVWarps * g) + rl;
+                        if (pw + kVWarps * g < 32) {
+                            vc[g] = *reinterpret_cast<const uint4*>(vq + row * 128 + 16 * ch);
+                            vd[g] = *reinterpret_cast<const __half*>(x.ph + PG::kOffVd + row * 8 + (ch & ~1));
+                        }
+                    }
+                } else if constexpr (VT != kVF16) {
+#pragma unroll
+                    for (int g = 0; g < kMine; ++g) {
+                        const int row = x.t0 + 8 * (pw + kVWarps * g) + rv;
+                        if (pw + kVWarps * g < 16) {
+                            vc[g] = *reinterpret_cast<const uint4*>(vq + row * 64 + 16 * bv);
+                            vd[g] = *reinterpret_cast<const __half*>(x.ph + PG::kOffVd + row * 8 + 2 * bv);
+                            if constexpr (v_has_fifth(VT)) vh[g] = *reinterpret_cast<const uint32_t*>(x.ph + PG::kOffVh + row * 16 + 4 * bv);
+                            if constexpr (v_has_min(VT)) vm[g] = *reinterpret_cast<const __half*>(x.ph + PG::kOffVm + row * 8 + 2 * bv);
+                        }
+                    }
+                }
+            };
+            Next x{nullptr, 0, 0, 0, false};
+            if (ok) x = advance();
+            if (x.there) load_v(x);
+            for (uint32_t n = 0; x.there; ++n) {
+                const Next y = advance();
+                const int vb = n & 1;
+                if (n >= 2) {
+                    wait(&v_free[vb], ((n >> 1) - 1) & 1);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                }
+                uint8_t* vt = smem + kOffV + vb * kTileBytes;
+                const __half zero = __float2half(0.0f);
+                if constexpr (VT == kVQ8_0) {
+#pragma unroll
+                    for (int g = 0; g < kMine; ++g) {
+                        const int row = 4 * (pw + kVWarps * g) + rl;
+                        if (pw + kVWarps * g < 32) {
+                            uint4 lo, hi;
+                            conv_s8(vc[g], h2u(__half2half2(row < x.valid ? vd[g] : zero)), lo, hi);
+                            st_chunk(vt, row, 2 * ch, lo);
+                            st_chunk(vt, row, 2 * ch + 1, hi);
+                        }
+                    }
+                } else if constexpr (VT == kVF16) {
+                    if (pw == 0 && lane == 0) {
+                        mbar_expect_tx(&v_raw[vb], kTileBytes);
+                        tma4(vt, &maps.v, 0, 0, PG::kOffVq / 256 + x.t0, x.hp, &v_raw[vb]);
+                        tma4(vt + 16384, &maps.v, 0, 1, PG::kOffVq / 256 + x.t0, x.hp, &v_raw[vb]);
+                    }
+                    wait(&v_raw[vb], (n >> 1) & 1);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    for (int c = pw * 32 + lane; x.valid < kStageKeys && c < 128 * 16; c += kVWarps * 32)
+                        if ((c >> 4) >= x.valid) st_chunk(vt, c >> 4, c & 15, make_uint4(0u, 0u, 0u, 0u));
+                } else {
+#pragma unroll
+                    for (int g = 0; g < kMine; ++g) {
+                        const int row = 8 * (pw + kVWarps * g) + rv;
+                        if (pw + kVWarps * g < 16) {
+                            const bool there = row < x.valid;
+                            const __half2 d = __half2half2(there ? vd[g] : zero);
+                            const __half2 m = v_has_min(VT) ? __half2half2(there ? vm[g] : zero) : __float2half2_rn(0.0f);
+                            constexpr float kZero = v_has_min(VT) ? 0.0f : (VT == kVQ5_0 ? 16.0f : 8.0f);
+                            const __half2 z = __float2half2_rn(1024.0f + kZero), z16 = __float2half2_rn(-64.0f - kZero);
+                            const __half2 sixteenth = __float2half2_rn(0.0625f);
+                            const uint32_t words[4] = {vc[g].x, vc[g].y, vc[g].z, vc[g].w};
+                            // dims 0..15 (low nibbles), 16..31 (high); of four dims the pairs are (0, 2) and
+                            // (1, 3), two masks instead of byte moves: O's columns come out in that order
+                            uint32_t o[2][8];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const uint32_t wd = e ? words[k] >> 8 : words[k];
+                                    uint32_t lo = (wd & 0x000f000fu) | 0x64006400u, hi = (wd & 0x00f000f0u) | 0x64006400u;
+                                    if constexpr (v_has_fifth(VT)) {
+                                        const uint32_t b = vh[g] >> (4 * k + e);  // bits 0, 2 and 16, 18
+                                        lo |= (b & 1u) << 4 | (b & 4u) << 18;
+                                        hi |= (b & 0x10000u) >> 8 | (b & 0x40000u) << 6;
+                                    }
+                                    const __half2 ql = __hsub2(u2h(lo), z), qh = __hfma2(u2h(hi), sixteenth, z16);
+                                    o[0][2 * k + e] = h2u(v_has_min(VT) ? __hfma2(ql, d, m) : __hmul2(ql, d));
+                                    o[1][2 * k + e] = h2u(v_has_min(VT) ? __hfma2(qh, d, m) : __hmul2(qh, d));
+                                }
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                st_chunk(vt, row, 4 * bv + c, make_uint4(o[c >> 1][4 * (c & 1)], o[c >> 1][4 * (c & 1) + 1],
+                                                                         o[c >> 1][4 * (c & 1) + 2], o[c >> 1][4 * (c & 1) + 3]));
+                        }
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) arrive(&k_full[kb]);
-                if (y.there) load_k(y);  // behind the fence, which waits for loads in flight
-            } else if (pw == 0 && lane == 0) {
-                mbar_expect_tx(&k_full[kb], kTileBytes);
-                tma4(kt, &maps.k, 0, 0, x.t0, x.hp, &k_full[kb]);
-                tma4(kt + 16384, &maps.k, 0, 1, x.t0, x.hp, &k_full[kb]);
+                if (lane == 0) arrive(&v_full[vb]);
+                if (y.there) load_v(y);
+                x = y;
             }
-            ++n_k;
-            // ---- V: rows that do not exist hold anything, their values become 0 ----
-            if (n_v >= 2) {
-                wait(&v_free[vb], ((n_v >> 1) - 1) & 1);
-                if (!__all_sync(0xffffffffu, ok)) break;
-            }
-            uint8_t* vt = smem + kOffV + vb * kTileBytes;
-            const __half zero = __float2half(0.0f);
-            if constexpr (VT == kVQ8_0) {
-#pragma unroll
-                for (int g = 0; g < kMineV; ++g) {
-                    const int row = 4 * (pw + kProdWarps * g) + rl;
-                    if (pw + kProdWarps * g < 32) {
-                        uint4 lo, hi;
-                        conv_s8(vc[g], h2u(__half2half2(row < x.valid ? vd[g] : zero)), lo, hi);
-                        st_chunk(vt, row, 2 * ch, lo);
-                        st_chunk(vt, row, 2 * ch + 1, hi);
-                    }
-                }
-            } else if constexpr (VT == kVF16) {
-                if (pw == 0 && lane == 0) {
-                    mbar_expect_tx(&v_raw[vb], kTileBytes);
-                    tma4(vt, &maps.v, 0, 0, PG::kOffVq / 256 + x.t0, x.hp, &v_raw[vb]);
-                    tma4(vt + 16384, &maps.v, 0, 1, PG::kOffVq / 256 + x.t0, x.hp, &v_raw[vb]);
-                }
-                wait(&v_raw[vb], (n_v >> 1) & 1);
-                if (!__all_sync(0xffffffffu, ok)) break;
-                for (int c = pw * 32 + lane; x.valid < kStageKeys && c < 128 * 16; c += kProdWarps * 32)
-                    if ((c >> 4) >= x.valid) st_chunk(vt, c >> 4, c & 15, make_uint4(0u, 0u, 0u, 0u));
-            } else {
-#pragma unroll
-                for (int g = 0; g < kMineV; ++g) {
-                    const int row = 8 * (pw + kProdWarps * g) + rv;
-                    if (pw + kProdWarps * g < 16) {
-                        const bool there = row < x.valid;
-                        const __half2 d = __half2half2(there ? vd[g] : zero);
-                        const __half2 m = v_has_min(VT) ? __half2half2(there ? vm[g] : zero) : __float2half2_rn(0.0f);
-                        constexpr float kZero = v_has_min(VT) ? 0.0f : (VT == kVQ5_0 ? 16.0f : 8.0f);
-                        const __half2 z = __float2half2_rn(1024.0f + kZero);
-                        const uint32_t words[4] = {vc[g].x, vc[g].y, vc[g].z, vc[g].w};
-                        uint32_t o[2][8];  // dims 0..15 (low nibbles), 16..31 (high), as pairs
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-#pragma unroll
-                            for (int n = 0; n < 2; ++n) {
-                                const uint32_t c4 = (n ? words[k] >> 4 : words[k]) & 0x0f0f0f0fu;
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    uint32_t q2 = __byte_perm(c4, 0x64646464u, e ? 0x4342 : 0x4140);
-                                    if constexpr (v_has_fifth(VT)) {
-                                        const int bit = 16 * n + 4 * k + 2 * e;
-                                        q2 |= ((vh[g] >> bit) & 1u) << 4 | ((vh[g] >> (bit + 1)) & 1u) << 20;
-                                    }
-                                    const __half2 q = __hsub2(u2h(q2), z);
-                                    o[n][2 * k + e] = h2u(v_has_min(VT) ? __hfma2(q, d, m) : __hmul2(q, d));
-                                }
-                            }
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            st_chunk(vt, row, 4 * bv + c, make_uint4(o[c >> 1][4 * (c & 1)], o[c >> 1][4 * (c & 1) + 1],
-                                                                     o[c >> 1][4 * (c & 1) + 2], o[c >> 1][4 * (c & 1) + 3]));
-                    }
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) arrive(&v_full[vb]);
-            if (y.there) load_v(y);
-            ++n_v;
-            x = y;
         }
     } else {
-        if (lane == 0) {
         // ============================ products ============================
+        const uint32_t one = elect_one();
+        const uint32_t smem0 = smem_u32(smem);
         uint32_t n_k = 0, n_v = 0, n_p[2] = {0, 0}, n_q[2] = {0, 0};
         for (long long cur = run0; ok && cur < run1 && walk_to(a, w, cur, n_groups);) {
             const long long stop = min(run1, w.unit0 + w.u.n_stages);
             const int n_st = (int)(stop - cur);
             const int tiles = w.u.rows > 128 ? 2 : 1;
             cur = stop;
-            auto scores = [&](int t, int kb) {
-                const uint32_t q = smem_u32(smem + kOffQ + t * kTileBytes), k = smem_u32(smem + kOffK + kb * kTileBytes);
+            auto scores = [&](int t, uint32_t kb) {
+                const uint32_t q = smem0 + kOffQ + t * kTileBytes, k = smem0 + kOffK + kb * kTileBytes;
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) tc_mma_f16(tmem + kColS + 128 * t, desc_k(q, kk), desc_k(k, kk), kIdescS, kk > 0);
-                tc_commit(&s_full[t]);
+                for (int kk = 0; kk < 8; ++kk) mma_ss(tmem + kColS + 128 * t, desc_k(q, kk), desc_k(k, kk), kIdescS, kk > 0, one);
+                commit_one(&s_full[t], one);
             };
-            if (!wait(&k_full[n_k & 1], (n_k >> 1) & 1)) break;
-            for (int t = 0; t < tiles && wait(&q_full[t], n_q[t] & 1); ++t) {
+            wait(&k_full[n_k & 1], (n_k >> 1) & 1);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (t >= tiles) break;
+                wait(&q_full[t], n_q[t] & 1);
+                if (!__all_sync(0xffffffffu, ok)) break;
                 ++n_q[t];
                 tc_fence_after();
                 scores(t, n_k & 1);
             }
-            if (!ok) break;
-            tc_commit(&k_free[n_k & 1]);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            commit_one(&k_free[n_k & 1], one);
             ++n_k;
-            for (int i = 0; i < n_st && ok; ++i) {
-                const int vb = n_v & 1;
-                if (!wait(&v_full[vb], (n_v >> 1) & 1)) break;
-                for (int t = 0; t < tiles; ++t) {
-                    if (!wait(&p_full[t], n_p[t] & 1)) break;
+            for (int i = 0; i < n_st; ++i) {
+                const uint32_t vb = n_v & 1;
+                wait(&v_full[vb], (n_v >> 1) & 1);
+                if (i + 1 < n_st) wait(&k_full[n_k & 1], (n_k >> 1) & 1);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (t >= tiles) break;
+                    wait(&p_full[t], n_p[t] & 1);
+                    if (!__all_sync(0xffffffffu, ok)) break;
                     ++n_p[t];
                     tc_fence_after();
-                    const uint32_t v = smem_u32(smem + kOffV + vb * kTileBytes);
+                    const uint32_t v = smem0 + kOffV + vb * kTileBytes;
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        mma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * kk, desc_mn(v, kk), kIdescPV, i > 0 || kk > 0);
-                    if (t == tiles - 1) tc_commit(&v_free[vb]);
+                        mma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * kk, desc_mn(v, kk), kIdescPV, i > 0 || kk > 0, one);
+                    if (t == tiles - 1) commit_one(&v_free[vb], one);
                     if (i + 1 < n_st) {
-                        if (t == 0 && !wait(&k_full[n_k & 1], (n_k >> 1) & 1)) break;
-                        tc_fence_after();
                         scores(t, n_k & 1);
-                        if (t == tiles - 1) {
-                            tc_commit(&k_free[n_k & 1]);
-                            ++n_k;
-                        }
+                        if (t == tiles - 1) commit_one(&k_free[n_k & 1], one);
                     } else {
-                        tc_commit(&o_full[t]);
+                        commit_one(&o_full[t], one);
                     }
                 }
+                if (!__all_sync(0xffffffffu, ok)) break;
+                if (i + 1 < n_st) ++n_k;
                 ++n_v;
             }
         }
         if (run0 < run1) {  // nothing is in flight when the memory is given back
-            tc_commit(done);
-            mbar_wait_bounded(done, 0, a.batch.status);
-        }
+            commit_one(done, one);
+            wait_phase(done, 0, a.batch.status);
         }
         __syncwarp();
     }
