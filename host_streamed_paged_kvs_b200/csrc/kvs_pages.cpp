@@ -135,7 +135,7 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 struct Workspace {
     size_t counters = 0, plan, units, records, prior_acc, prior_ml, bytes;
     Workspace(long long n_rows, long long n_seqs, long long n_qh, int group) {
-        const bool wide = n_rows * group > kFewRowsMax;
+        const bool wide = n_rows * group > kFewSeqRows;
         plan = up256((size_t)kFewCtas * sizeof(int));
         units = plan + up256(sizeof(WidePlan));
         records = units + (wide ? up256((size_t)wide_groups(n_rows, group, n_seqs) * sizeof(WideUnit)) : 0);
@@ -269,22 +269,22 @@ extern "C" int kvs_attend_pages(const kvs_page_pool* pool, const kvs_page_batch*
     // Up to 32 rows per kv head go to the few-row kernel (HBM bound, fp32-class
     // sums), more to the tensor-core kernel.
     auto few = [&](AttendPagesArgs& x, long long rows) {
-        return launched(launch_attend_few(x, maps, rows <= 8 ? 8 : (rows <= 16 ? 16 : kFewRowsMax), n_sms, s));
+        return launched(launch_attend_few(x, maps, rows <= 8 ? 8 : kFewRowsMax, n_sms, s));
     };
     const long long all = (long long)a.batch.n_rows * a.group;
     if (a.prefix_len > 0) {
         AttendPagesArgs p = a;
         p.prefix_phase = 1;
-        rc = all > kFewRowsMax ? launched(launch_attend_wide(p, maps, n_sms, s)) : few(p, all);
+        rc = all > kFewSeqRows ? launched(launch_attend_wide(p, maps, n_sms, s)) : few(p, all);
         if (rc != KVS_OK) return rc;
     }
     const long long most = (batch->max_new > 0 && batch->max_new < a.batch.n_rows ? batch->max_new : a.batch.n_rows) * (long long)a.group;
-    if (most <= kFewRowsMax) {
+    if (most <= kFewSeqRows) {
         a.few_rows = 0x7fffffff;
         return few(a, most);
     }
-    a.few_rows = a.batch.n_seqs == 1 ? 0 : kFewRowsMax;
+    a.few_rows = a.batch.n_seqs == 1 ? 0 : kFewSeqRows;
     rc = launched(launch_attend_wide(a, maps, n_sms, s));
-    if (rc == KVS_OK && a.few_rows > 0) rc = few(a, 8);
+    if (rc == KVS_OK && a.few_rows > 0) rc = few(a, a.group);  // single tokens beside prompts
     return rc;
 }

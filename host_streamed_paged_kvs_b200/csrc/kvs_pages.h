@@ -102,10 +102,11 @@ inline long long wide_groups(long long n_rows, int group, long long n_seqs) {
     return n_rows * group / kWideRows + n_seqs + 1;
 }
 
-// rows of a unit of the few-row kernel: 8, 16 or 32
-constexpr int kFewRowsMax = 32;
+// a unit of the few-row kernel has 8 or 16 rows; a sequence of up to 32 rows is one or two units
+constexpr int kFewRowsMax = 16;
+constexpr int kFewSeqRows = 32;
 constexpr int kRecordFloats = 132;      // 128 sums, reference, sum of weights, padding
-constexpr int kFewCtas = 296;           // two per SM
+constexpr int kFewCtas = 444;           // up to three per SM
 constexpr size_t kFewRecordBytes = (size_t)kFewCtas * 2 * kFewRowsMax * kRecordFloats * 4;
 
 struct PageMaps {

@@ -54,6 +54,7 @@ namespace {
 constexpr int kConsumers = 4;
 constexpr int kThreads = (kConsumers + 1) * 32;
 constexpr int kStageKeys = 128;
+constexpr int kLeastStages = 1;                    // a CTA's run
 constexpr int kQRow = 288;                         // bytes of a Q row in shared memory: 32 mod 128, so that 4 rows x 32 B are distinct banks
 constexpr int kRedRow = 132;                       // floats of a row in the join buffer
 constexpr int kRedBytes = kConsumers * 8 * kRedRow * 4;
@@ -86,7 +87,7 @@ struct Geo {
     static constexpr int kOffVm = kOffVd + kStageKeys * PG::kVdRow;
     static constexpr int kBytes = kOffVm + kStageKeys * PG::kVmRow;
     static constexpr size_t kFixed = 1024 + kRedBytes + 2 * sizeof(Piece<kRows>) + 512;
-    static constexpr int kPerSm = NT <= 2 && 2 * (2 * (size_t)kBytes + kFixed + 1024) <= 233472 ? 2 : 1;
+    static constexpr int kPerSm = 2 * (2 * (size_t)kBytes + kFixed + 1024) <= 233472 ? 2 : 1;
     static constexpr int kFit = (int)((233472 / kPerSm - 1024 - kFixed) / kBytes);
     static constexpr int kStages = kFit < 4 ? kFit : 4;
     static constexpr size_t kOffRed = (size_t)kStages * kBytes;
@@ -179,29 +180,34 @@ __device__ __forceinline__ Seq seq_of(const AttendPagesArgs& a, int i) {
     return s;
 }
 
-template <int VT, int KT, int NT>
+// a / b for a >= 0, b > 0: 32-bit where both fit
+__device__ __forceinline__ long long quot(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// PRECISE: the weights' rounding errors go in as a second term (a template
+// argument: the branches would keep the compiler from overlapping the blocks)
+template <int VT, int KT, int NT, bool PRECISE>
 __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
     attend_few_kernel(const __grid_constant__ AttendPagesArgs a, const __grid_constant__ PageMaps maps) {
     using G = Geo<VT, KT, NT>;
     using PG = PageGeom<VT, KT>;
     constexpr int ROWS = G::kRows, kStages = G::kStages;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    // aligned by an offset, not through an integer: a pointer made from an integer is
+    // a generic one, and every access to it a generic load or store
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     float* red = reinterpret_cast<float*>(smem + G::kOffRed);
     Piece<ROWS>* pieces = reinterpret_cast<Piece<ROWS>*>(smem + G::kOffPiece);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::kOffBar);  // [stage] bytes landed
     uint64_t* empty = full + kStages;                                 // [stage] consumers done
     uint64_t* p_full = empty + kStages;                               // [piece slot] published
     uint64_t* p_empty = p_full + 2;                                   // [piece slot] consumers done
-    uint64_t* c_bar = p_empty + 2;                                    // the consumers' own barrier
-    long long* sScan = reinterpret_cast<long long*>(c_bar + 1);       // [kConsumers + 1] warp sums
-    long long* sBase = sScan + 8;                                     // stages before the first sequence
-    int* sSeq = reinterpret_cast<int*>(sBase + 1);                    // first sequence of the run
-    int* sLast = sSeq + 1;                                            // this CTA joins the unit
-    float* sml = reinterpret_cast<float*>(sSeq + 4);                  // [warp][8][2] (reference, sum)
+    int* sLast = reinterpret_cast<int*>(p_empty + 2);                 // this CTA joins the unit
+    float* sml = reinterpret_cast<float*>(p_empty + 4);               // [warp][8][2] (reference, sum)
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int n_units_of = a.pool.n_kv;
+    const int n_kv = a.pool.n_kv;
     const int n_seqs = a.prefix_phase ? 1 : a.batch.n_seqs;
 
     if (tid == 0) {
@@ -213,73 +219,53 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
             mbar_init(&p_full[s], 1);
             mbar_init(&p_empty[s], kConsumers);
         }
-        mbar_init(c_bar, kConsumers);
         fence_mbar_init();
-        *sSeq = n_seqs;
     }
+    __syncthreads();
 
-    // ---- this CTA's run of the list of all units' stages ----
-    long long total = 0;
-    {
-        long long mine = 0;
-        for (int i = tid; i < n_seqs; i += kThreads) {
+    if (warp == kConsumers) {
+        // ============================ producer ============================
+        // ---- this CTA's run of the list of all units' stages: the sequences' shares,
+        // 32 at a time, summed once for the whole and once up to the run's start ----
+        auto share = [&](int i) -> long long {
+            if (i >= n_seqs) return 0;
             const Seq s = seq_of<ROWS>(a, i);
-            mine += s.n_stages * s.n_groups * n_units_of;
-        }
+            return s.n_stages * s.n_groups * n_kv;
+        };
+        const long long mine = share(lane);  // of the first 32, which are all of most batches
+        long long total = mine;
+        for (int i = 32 + lane; i < n_seqs; i += 32) total += share(i);
 #pragma unroll
-        for (int off = 16; off; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
-        if (lane == 0) sScan[warp] = mine;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) total += sScan[w];
-        __syncthreads();
-    }
-    const long long per = max(1ll, (total + gridDim.x - 1) / gridDim.x);
-    const long long run0 = min(total, per * blockIdx.x), run1 = min(total, run0 + per);
-    if (run0 >= run1) return;
-    {
-        long long before = 0;
-        for (int i0 = 0; i0 < n_seqs && before <= run0; i0 += kThreads) {
-            const int i = i0 + tid;
-            long long cost = 0;
-            if (i < n_seqs) {
-                const Seq s = seq_of<ROWS>(a, i);
-                cost = s.n_stages * s.n_groups * n_units_of;
-            }
-            long long upto = cost;
+        for (int off = 16; off; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+        const long long per = max((long long)kLeastStages, quot(total + gridDim.x - 1, gridDim.x));
+        const long long run0 = min(total, per * blockIdx.x), run1 = min(total, run0 + per);
+        int seq = n_seqs;
+        long long base = 0;
+        for (int i0 = 0; i0 < n_seqs && run0 < run1; i0 += 32) {
+            const long long own = i0 == 0 ? mine : share(i0 + lane);
+            long long upto = own;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const long long v = __shfl_up_sync(0xffffffffu, upto, off);
                 if (lane >= off) upto += v;
             }
-            if (lane == 31) sScan[warp] = upto;
-            __syncthreads();
-            long long all = 0;
-#pragma unroll
-            for (int w = 0; w < kThreads / 32; ++w) {
-                if (w < warp) upto += sScan[w];
-                all += sScan[w];
+            upto += base;
+            const uint32_t past = __ballot_sync(0xffffffffu, upto > run0);
+            if (past) {  // the first sequence whose shares pass the run's start
+                const int at = __ffs(past) - 1;
+                seq = i0 + at;
+                base = __shfl_sync(0xffffffffu, upto - own, at);
+                break;
             }
-            upto += before;
-            if (upto - cost <= run0 && run0 < upto) {
-                *sSeq = i;
-                *sBase = upto - cost;
-            }
-            before += all;
-            __syncthreads();
+            base = __shfl_sync(0xffffffffu, upto, 31);
         }
-    }
-
-    if (warp == kConsumers) {
-        // ============================ producer ============================
-        int seq = *sSeq;
-        long long base = *sBase, cur = run0;
+        long long cur = run0;
         int issued = 0, n_pieces = 0;
         bool ok = true;
         Seq s = seq < n_seqs ? seq_of<ROWS>(a, seq) : Seq{};
         while (ok) {
-            while (seq < n_seqs && cur < run1 && cur >= base + s.n_stages * s.n_groups * n_units_of) {
-                base += s.n_stages * s.n_groups * n_units_of;
+            while (seq < n_seqs && cur < run1 && cur >= base + s.n_stages * s.n_groups * n_kv) {
+                base += s.n_stages * s.n_groups * n_kv;
                 ++seq;
                 if (seq < n_seqs) s = seq_of<ROWS>(a, seq);
             }
@@ -291,10 +277,10 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                 if (lane == 0) arrive(&p_full[n_pieces & 1]);
                 break;
             }
-            const long long unit = (cur - base) / s.n_stages;
+            const long long unit = quot(cur - base, s.n_stages);
             const long long unit0 = base + unit * s.n_stages, unit1 = unit0 + s.n_stages;
             const long long stop = min(run1, unit1);
-            const int group = (int)(unit / n_units_of), h = (int)(unit % n_units_of);
+            const int group = (int)quot(unit, n_kv), h = (int)(unit - (long long)group * n_kv);
             const int rows = min(ROWS, s.rows * a.group - group * ROWS);
             // bounds of the rows, one lane each
             int first = INT_MAX, end = 0, pos = 0, token = -1, head = 0;
@@ -350,47 +336,14 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                 p.full_from = full_from;
                 p.full_to = full_to;
                 p.n_keys = s.n_keys;
-                p.slot = (unit0 >= run0 && unit1 <= run1) ? -1 : (unit0 < run0 ? 0 : 1);
-                p.cta0 = (int)(unit0 / per);
-                p.n_ctas = (int)((unit1 - 1) / per) - p.cta0 + 1;
                 // a row that may see keys beyond the page table
                 p.bad = hi > (long long)a.batch.table_stride * kPageTokens && !a.prefix_phase;
             }
-            // Q: fp16 as it is; bf16 as fp16 after taking each row's power of two
-            // out (exact down to 2^-24 of the row's largest value)
-            const float unit_scale = a.softcap > 0.0f || a.slopes ? a.scale : a.scale * 1.4426950408889634f;
-#pragma unroll 4
-            for (int r = 0; r < ROWS; ++r) {
-                const int tk = __shfl_sync(0xffffffffu, token, r), hd = __shfl_sync(0xffffffffu, head, r);
-                uint2 w = make_uint2(0u, 0u);
-                if (tk >= 0)
-                    w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q.p) + tk * a.q.row + hd * a.q.head + 4 * lane);
-                float sc = unit_scale;
-                if (a.q_dtype == kDtBF16) {
-                    const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
-                    const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
-                    float top = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y)));
-#pragma unroll
-                    for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                    // 2^e with 2^e <= top < 2^(e+1); 1 for zero, subnormal and non-finite rows
-                    const uint32_t ex = (__float_as_uint(top) >> 23) & 0xffu;
-                    const bool plain = ex < 2 || ex > 252;
-                    const float up = plain ? 1.0f : __uint_as_float(ex << 23), down = plain ? 1.0f : __uint_as_float((254u - ex) << 23);
-                    *reinterpret_cast<__half2*>(&w.x) = __floats2half2_rn(x.x * down, x.y * down);
-                    *reinterpret_cast<__half2*>(&w.y) = __floats2half2_rn(y.x * down, y.y * down);
-                    sc *= up;
-                }
-                *reinterpret_cast<uint2*>(p.q + r * kQRow + 8 * lane) = w;
-                if (lane == 0) p.scale[r] = sc;
-            }
-            __syncwarp();
-            if (lane == 0) arrive(&p_full[n_pieces & 1]);
-
-            // ---- the piece's stages ----
+            // ---- the piece's stages: 128 keys each ----
             const int* table = a.prefix_phase ? a.prefix_table : a.batch.table + (size_t)seq * a.batch.table_stride;
             const int n_table = a.prefix_phase ? (a.prefix_len + kPageTokens - 1) / kPageTokens : a.batch.table_stride;
             int pages = 0, pages_at = -1;  // 32 page numbers, one a lane
-            for (int st = st0; st < st1; ++st) {
+            auto issue = [&](int st) -> bool {
                 const int j = st >> 1;
                 if (pages_at < 0 || j >= pages_at + 32) {
                     pages_at = j;
@@ -399,10 +352,8 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                 int page = __shfl_sync(0xffffffffu, pages, j - pages_at);
                 const int buf = issued % kStages;
                 if (issued >= kStages &&
-                    !wait_phase(&empty[buf], ((issued / kStages) - 1) & 1, a.batch.status)) {
-                    ok = false;
-                    break;
-                }
+                    !wait_phase(&empty[buf], ((issued / kStages) - 1) & 1, a.batch.status))
+                    return false;
                 if (lane == 0) {
                     if ((unsigned)page >= (unsigned)a.pool.n_pages) {
                         page = 0;  // some page: its piece comes out as NaN
@@ -434,7 +385,53 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                 }
                 __syncwarp();
                 ++issued;
+                return true;
+            };
+            // the first stages' copies start before Q, which takes a while itself; they
+            // wait for no buffer but one that the piece before is done with
+            int st = st0;
+            for (; st < st1 && st < st0 + kStages; ++st) {
+                const bool free = issued < kStages || mbar_try_wait(&empty[issued % kStages], ((issued / kStages) - 1) & 1);
+                if (!__all_sync(0xffffffffu, free)) break;
+                issue(st);
             }
+            if (lane == 0) {
+                // the record slot, and the CTAs that share the unit
+                p.slot = (unit0 >= run0 && unit1 <= run1) ? -1 : (unit0 < run0 ? 0 : 1);
+                p.cta0 = unit0 >= run0 ? (int)blockIdx.x : (int)quot(unit0, per);
+                p.n_ctas = (unit1 <= run1 ? (int)blockIdx.x : (int)quot(unit1 - 1, per)) - p.cta0 + 1;
+            }
+            // Q: fp16 as it is; bf16 as fp16 after taking each row's power of two
+            // out (exact down to 2^-24 of the row's largest value)
+            const float unit_scale = a.softcap > 0.0f || a.slopes ? a.scale : a.scale * 1.4426950408889634f;
+#pragma unroll 8
+            for (int r = 0; r < ROWS; ++r) {
+                const int tk = __shfl_sync(0xffffffffu, token, r), hd = __shfl_sync(0xffffffffu, head, r);
+                uint2 w = make_uint2(0u, 0u);
+                if (tk >= 0)
+                    w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q.p) + tk * a.q.row + hd * a.q.head + 4 * lane);
+                float sc = unit_scale;
+                if (a.q_dtype == kDtBF16) {
+                    const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
+                    const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
+                    float top = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y)));
+#pragma unroll
+                    for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                    // 2^e with 2^e <= top < 2^(e+1); 1 for zero, subnormal and non-finite rows
+                    const uint32_t ex = (__float_as_uint(top) >> 23) & 0xffu;
+                    const bool plain = ex < 2 || ex > 252;
+                    const float up = plain ? 1.0f : __uint_as_float(ex << 23), down = plain ? 1.0f : __uint_as_float((254u - ex) << 23);
+                    *reinterpret_cast<__half2*>(&w.x) = __floats2half2_rn(x.x * down, x.y * down);
+                    *reinterpret_cast<__half2*>(&w.y) = __floats2half2_rn(y.x * down, y.y * down);
+                    sc *= up;
+                }
+                *reinterpret_cast<uint2*>(p.q + r * kQRow + 8 * lane) = w;
+                if (lane == 0) p.scale[r] = sc;
+            }
+            __syncwarp();
+            if (lane == 0) arrive(&p_full[n_pieces & 1]);
+
+            for (; ok && st < st1; ++st) ok = __all_sync(0xffffffffu, issue(st));
             cur = stop;
             ++n_pieces;
         }
@@ -447,21 +444,29 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
     // ============================ consumers ============================
     const int g = lane >> 2, q = lane & 3;
     const bool formed = a.softcap > 0.0f || a.slopes;  // scores need more than a scale
-    int used = 0;                                      // stages so far
-    // a barrier of the four consumer warps whose wait is bounded like every other
-    // here: a warp whose wait gave up leaves nobody behind for good
-    uint32_t c_phase = 0;
+    int buf = 0;                                       // the next stage's buffer and its phase
+    uint32_t buf_phase = 0;
+    // The barrier of the four consumer warps says whether a bounded wait of any of
+    // them gave up; all leave then.  A warp whose wait failed still comes to the
+    // next barrier, and so does one that has reached the end, so nobody is left.
+    bool ok = true;
     auto consumers_sync = [&]() -> bool {
-        __syncwarp();
-        if (lane == 0) arrive(c_bar);
-        const bool ok = wait_phase(c_bar, c_phase, a.batch.status);
-        c_phase ^= 1;
-        return __all_sync(0xffffffffu, ok);
+        int lost;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %1, 0;\n\tbarrier.cta.red.or.pred p, 1, 128, q;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+            : "=r"(lost)
+            : "r"(ok ? 0 : 1)
+            : "memory");
+        return lost == 0;
     };
     for (int n = 0;; ++n) {
         Piece<ROWS>& p = pieces[n & 1];
-        if (!wait_phase(&p_full[n & 1], (n >> 1) & 1, a.batch.status)) return;
-        if (p.n_stages < 0) return;
+        ok = wait_phase(&p_full[n & 1], (n >> 1) & 1, a.batch.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok || p.n_stages < 0) {
+            consumers_sync();
+            return;
+        }
         float o[8][NT][4];
         float ref[NT][2], l[NT][2], sc[NT][2];
 #pragma unroll
@@ -478,11 +483,11 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
             }
         }
         const uint8_t* sq = p.q + g * kQRow + 8 * q;  // this lane's operand: row g, dims 16 c + 4 q ..
-        bool ok = true;
-        for (int i = 0; i < p.n_stages; ++i, ++used) {
-            const int buf = used % kStages;
-            ok = wait_phase(&full[buf], (used / kStages) & 1, a.batch.status);
-            if (!__all_sync(0xffffffffu, ok)) return;
+        const int n_stages = p.n_stages;
+        for (int i = 0; i < n_stages; ++i) {
+            ok = wait_phase(&full[buf], buf_phase, a.batch.status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
             const uint8_t* sb = smem + buf * G::kBytes;
             const int key0 = (p.first_stage + i) * kStageKeys;  // the stage's first key
             const int wk = warp * 32;                           // this warp's first key in it
@@ -519,12 +524,6 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                     }
                 }
             } else {
-                uint2 kd[2][2];  // the four block scales of keys g, g + 8 of each tile
-#pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        kd[mt][j] = *reinterpret_cast<const uint2*>(sb + G::kOffKd + (wk + 16 * mt + 8 * j + g) * 8);
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b) {
                     uint2 qb[NT][2];
@@ -542,9 +541,8 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                         s8x4(w[1], 0x4140, 0x4342, k0[1], k0[3]);
                         s8x4(w[2], 0x4140, 0x4342, k1[0], k1[2]);
                         s8x4(w[3], 0x4140, 0x4342, k1[1], k1[3]);
-                        const __half2 d0 = u2h(b < 2 ? kd[mt][0].x : kd[mt][0].y), d1 = u2h(b < 2 ? kd[mt][1].x : kd[mt][1].y);
-                        const float f0 = (b & 1) ? __high2float(d0) : __low2float(d0);
-                        const float f1 = (b & 1) ? __high2float(d1) : __low2float(d1);
+                        const __half* kd = reinterpret_cast<const __half*>(sb + G::kOffKd + (wk + 16 * mt + g) * 8) + b;
+                        const float f0 = __half2float(kd[0]), f1 = __half2float(kd[8 * kBlocks]);  // keys g, g + 8
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -639,22 +637,33 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                 }
 
             // ---- O^T += V^T P^T, 16 keys at a time ----
+            // weights with keys along the pair: [tile][nt][keys 2q,2q+1 | 8+2q, 8+2q+1],
+            // and what their rounding to fp16 left
+            uint32_t ph2[2][NT][2], pl2[2][NT][2];
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-                // weights with keys along the pair: [nt][keys 2q,2q+1 | 8+2q, 8+2q+1], and
-                // what their rounding to fp16 left
-                uint32_t ph[NT][2], pl[NT][2];
+            for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int jk = 0; jk < 2; ++jk) {
                         const float x = s[mt][nt][2 * jk], y = s[mt][nt][2 * jk + 1];
                         const __half2 hi = __floats2half2_rn(x, y);
-                        ph[nt][jk] = movm(h2u(hi));
-                        if (a.precise) {
+                        ph2[mt][nt][jk] = movm(h2u(hi));
+                        pl2[mt][nt][jk] = 0u;
+                        if constexpr (PRECISE) {
                             const float2 f = __half22float2(hi);
-                            pl[nt][jk] = movm(h2u(__floats2half2_rn(x - f.x, y - f.y)));
+                            pl2[mt][nt][jk] = movm(h2u(__floats2half2_rn(x - f.x, y - f.y)));
                         }
+                    }
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+                uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int jk = 0; jk < 2; ++jk) {
+                        ph[nt][jk] = mt ? ph2[1][nt][jk] : ph2[0][nt][jk];
+                        pl[nt][jk] = mt ? pl2[1][nt][jk] : pl2[0][nt][jk];
                     }
                 // keys that do not exist hold anything: their scales (or values) become 0
                 uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
@@ -700,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                             } else {
                                 const __half2 hi = __hmul2(u2h(ph[nt][jk]), dvp[jk]);
                                 bh[nt][jk] = h2u(hi);
-                                if (a.precise)  // the product's own error (exact by fma) and the low term
+                                if constexpr (PRECISE)  // the product's own error (exact by fma) and the low term
                                     bl[nt][jk] = h2u(__hfma2(u2h(pl[nt][jk]), dvp[jk], __hfma2(u2h(ph[nt][jk]), dvp[jk], __hneg2(hi))));
                             }
                         }
@@ -771,19 +780,39 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             mma(o[2 * b + e][nt], va[e], bh[nt][0], bh[nt][1]);
-                            if (a.precise) mma(o[2 * b + e][nt], va[e], bl[nt][0], bl[nt][1]);
+                            if constexpr (PRECISE) mma(o[2 * b + e][nt], va[e], bl[nt][0], bl[nt][1]);
                         }
                 }
             }
             __syncwarp();
             if (lane == 0) arrive(&empty[buf]);
+            if (++buf == kStages) {
+                buf = 0;
+                buf_phase ^= 1;
+            }
         }
 
         // ---- the piece's end ----
         const bool bad = p.bad;
         if (bad && tid == 0 && a.batch.status) atomicOr(a.batch.status, kErrBadPage);
-        // joins the four warps' sums of rows 8 nt .. + 7 from the join buffer; two rows a
-        // warp, lane = dims 4 lane .. + 3
+        // What the prefix left for this warp's two rows of 8 nt .. + 7, on its way early
+        float4 pacc[2];
+        float2 pml[2];
+        auto fetch_prior = [&](int nt) {
+#pragma unroll
+            for (int rr = 0; rr < 2; ++rr) {
+                const int pr = 8 * nt + warp + kConsumers * rr;
+                pml[rr] = make_float2(-CUDART_INF_F, 0.0f);
+                pacc[rr] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (!a.prefix_phase && a.prefix_len > 0 && pr < p.rows && p.token[pr] >= 0) {
+                    const size_t at = (size_t)p.token[pr] * a.n_qh + p.head[pr];
+                    pml[rr] = a.prior_ml[at];
+                    pacc[rr] = reinterpret_cast<const float4*>(a.prior_acc)[at * 32 + lane];
+                }
+            }
+        };
+        // joins the four warps' sums of those rows from the join buffer, lane = dims
+        // 4 lane .. + 3, and ends them or keeps the CTA's record
         auto join_warps = [&](int nt, bool record) {
 #pragma unroll
             for (int rr = 0; rr < 2; ++rr) {
@@ -796,7 +825,8 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                     join(acc, M, L, *reinterpret_cast<const float4*>(red + (w * 8 + r) * kRedRow + 4 * lane), sml[(w * 8 + r) * 2],
                          sml[(w * 8 + r) * 2 + 1]);
                 if (!record) {
-                    finish_row<VT, KT>(a, p.seq, p.token[pr], p.head[pr], acc, M, L);
+                    join(acc, M, L, pacc[rr], pml[rr].x, pml[rr].y);
+                    end_row<VT, KT>(a, p.seq, p.token[pr], p.head[pr], acc, M, L);
                 } else {
                     float* rec = a.records + ((size_t)(blockIdx.x * 2 + p.slot) * kFewRowsMax + pr) * kRecordFloats;
                     *reinterpret_cast<float4*>(rec + 4 * lane) = acc;
@@ -807,6 +837,7 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             if (8 * nt >= p.rows) break;  // uniform
+            if (p.slot < 0) fetch_prior(nt);
 #pragma unroll
             for (int jr = 0; jr < 2; ++jr) {
                 float sum = l[nt][jr];
@@ -834,44 +865,45 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
         }
         if (p.slot >= 0) {
             // ---- a shared unit: the last CTA to arrive joins the records.  Each warp
-            // takes every fourth record, two rows and eight records in flight ----
-            __threadfence();
+            // takes every fourth record, four rows of four records in flight
+            // (the barrier orders the warps' records before the thread's release) ----
             if (!consumers_sync()) return;
             if (tid == 0) {
-                const int before = atomicAdd(&a.counters[p.cta0], 1);
+                int before;
+                asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(a.counters + p.cta0) : "memory");
                 const bool last = before == p.n_ctas - 1;
                 if (last) a.counters[p.cta0] = 0;  // ready for the next call
                 *sLast = last;
             }
             if (!consumers_sync()) return;
             if (*sLast) {
-                __threadfence();
                 const int n = p.n_ctas, cta0 = p.cta0, rows = p.rows;
-                constexpr int kBatch = 8;
+                constexpr int kRec = 4, kRow = 4;
 #pragma unroll 1
                 for (int nt = 0; 8 * nt < rows; ++nt) {
+                    fetch_prior(nt);
 #pragma unroll 1
-                    for (int r0 = 0; r0 < 8 && 8 * nt + r0 < rows; r0 += 2) {
-                        float4 acc[2];
-                        float M[2], L[2];
+                    for (int r0 = 0; r0 < 8 && 8 * nt + r0 < rows; r0 += kRow) {
+                        float4 acc[kRow];
+                        float M[kRow], L[kRow];
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
+                        for (int k = 0; k < kRow; ++k) {
                             acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                             M[k] = -CUDART_INF_F;
                             L[k] = 0.0f;
                         }
 #pragma unroll 1
-                        for (int c0 = warp; c0 < n; c0 += kConsumers * kBatch) {
-                            float4 v[kBatch][2];
-                            float2 ml[kBatch][2];
+                        for (int c0 = warp; c0 < n; c0 += kConsumers * kRec) {
+                            float4 v[kRec][kRow];
+                            float2 ml[kRec][kRow];
 #pragma unroll
-                            for (int b = 0; b < kBatch; ++b) {
+                            for (int b = 0; b < kRec; ++b) {
                                 const int c = c0 + kConsumers * b;
                                 // the first CTA began the unit, the others continue it
                                 const float* rec = a.records +
                                     ((size_t)((cta0 + min(c, n - 1)) * 2 + (c == 0 ? 1 : 0)) * kFewRowsMax + 8 * nt + r0) * kRecordFloats;
 #pragma unroll
-                                for (int k = 0; k < 2; ++k) {
+                                for (int k = 0; k < kRow; ++k) {
                                     v[b][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                                     ml[b][k] = make_float2(-CUDART_INF_F, 0.0f);
                                     if (c < n && 8 * nt + r0 + k < rows) {
@@ -881,12 +913,12 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                                 }
                             }
 #pragma unroll
-                            for (int b = 0; b < kBatch; ++b)
+                            for (int b = 0; b < kRec; ++b)
 #pragma unroll
-                                for (int k = 0; k < 2; ++k) join(acc[k], M[k], L[k], v[b][k], ml[b][k].x, ml[b][k].y);
+                                for (int k = 0; k < kRow; ++k) join(acc[k], M[k], L[k], v[b][k], ml[b][k].x, ml[b][k].y);
                         }
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
+                        for (int k = 0; k < kRow; ++k) {
                             *reinterpret_cast<float4*>(red + (warp * 8 + r0 + k) * kRedRow + 4 * lane) = acc[k];
                             if (lane == 0) {
                                 sml[(warp * 8 + r0 + k) * 2] = M[k];
@@ -905,7 +937,7 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
     }
 }
 
-template <int VT, int KT, int NT>
+template <int VT, int KT, int NT, bool PRECISE>
 cudaError_t launch(const AttendPagesArgs& a, const PageMaps& maps, int n_sms, cudaStream_t s) {
     using G = Geo<VT, KT, NT>;
     // the shared-memory opt-in is per device
@@ -913,21 +945,19 @@ cudaError_t launch(const AttendPagesArgs& a, const PageMaps& maps, int n_sms, cu
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !(configured.load(std::memory_order_acquire) & (1ull << dev))) {
-        const cudaError_t e = cudaFuncSetAttribute(attend_few_kernel<VT, KT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::kSmem);
+        const cudaError_t e = cudaFuncSetAttribute(attend_few_kernel<VT, KT, NT, PRECISE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::kSmem);
         if (e != cudaSuccess) return e;
         if (dev < 64) configured.fetch_or(1ull << dev, std::memory_order_acq_rel);
     }
-    attend_few_kernel<VT, KT, NT><<<std::min(kFewCtas, n_sms * G::kPerSm), kThreads, G::kSmem, s>>>(a, maps);
+    attend_few_kernel<VT, KT, NT, PRECISE><<<std::min(kFewCtas, n_sms * G::kPerSm), kThreads, G::kSmem, s>>>(a, maps);
     return cudaGetLastError();
 }
 
 template <int VT, int KT>
 cudaError_t by_rows(const AttendPagesArgs& a, const PageMaps& maps, int unit_rows, int n_sms, cudaStream_t s) {
-    switch (unit_rows) {
-        case 8: return launch<VT, KT, 1>(a, maps, n_sms, s);
-        case 16: return launch<VT, KT, 2>(a, maps, n_sms, s);
-        default: return launch<VT, KT, 4>(a, maps, n_sms, s);
-    }
+    if (unit_rows <= 8)
+        return a.precise ? launch<VT, KT, 1, true>(a, maps, n_sms, s) : launch<VT, KT, 1, false>(a, maps, n_sms, s);
+    return a.precise ? launch<VT, KT, 2, true>(a, maps, n_sms, s) : launch<VT, KT, 2, false>(a, maps, n_sms, s);
 }
 
 }  // namespace

@@ -154,20 +154,17 @@ __device__ __forceinline__ void join(float4& acc, float& M, float& L, const floa
 }
 
 // The end of one row, by a whole warp: lane holds sums of dims 4 lane .. + 3
-// relative to 2^M, L the sum of weights (0: the row sees nothing).  The prefix
-// phase keeps the record; the own phase joins it, divides and writes.
+// relative to 2^M, L the sum of weights (0: the row sees nothing), the prefix's
+// part joined.  The prefix phase keeps the record, the own phase divides and
+// writes.
 template <int VT, int KT>
-__device__ __forceinline__ void finish_row(const AttendPagesArgs& a, int seq, int row, int head, float4 acc, float M, float L) {
+__device__ __forceinline__ void end_row(const AttendPagesArgs& a, int seq, int row, int head, const float4& acc, float M, float L) {
     const int lane = threadIdx.x & 31;
     const size_t at = (size_t)row * a.n_qh + head;
     if (a.prefix_phase) {
         reinterpret_cast<float4*>(a.prior_acc)[at * 32 + lane] = acc;
         if (lane == 0) a.prior_ml[at] = make_float2(M, L);
         return;
-    }
-    if (a.prefix_len > 0) {
-        const float2 ml = a.prior_ml[at];
-        join(acc, M, L, reinterpret_cast<const float4*>(a.prior_acc)[at * 32 + lane], ml.x, ml.y);
     }
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (L != 0.0f) {
@@ -179,6 +176,17 @@ __device__ __forceinline__ void finish_row(const AttendPagesArgs& a, int seq, in
     }
     store_out4(a, row, head, 4 * lane, o);
     if (a.lse && lane == 0) a.lse[at] = L == 0.0f ? -CUDART_INF_F : (M + log2f(L)) * 0.69314718055994531f;
+}
+
+// The same, with the prefix's part fetched here.
+template <int VT, int KT>
+__device__ __forceinline__ void finish_row(const AttendPagesArgs& a, int seq, int row, int head, float4 acc, float M, float L) {
+    if (!a.prefix_phase && a.prefix_len > 0) {
+        const size_t at = (size_t)row * a.n_qh + head;
+        const float2 ml = a.prior_ml[at];
+        join(acc, M, L, reinterpret_cast<const float4*>(a.prior_acc)[at * 32 + (threadIdx.x & 31)], ml.x, ml.y);
+    }
+    end_row<VT, KT>(a, seq, row, head, acc, M, L);
 }
 
 }  // namespace kvs

@@ -327,7 +327,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     using PG = PageGeom<VT, KT>;
     constexpr bool kNibbles = VT != kVF16 && VT != kVQ8_0;  // O's columns: dims 0, 2, 1, 3 of every four
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    // aligned by an offset, not through an integer: a pointer made from an integer is
+    // a generic one, and every access to it a generic load or store
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
     uint64_t* k_full = bars;        // [buffer] K written (a producer warp each; TMA for fp16 K)
     uint64_t* k_free = bars + 2;    // [buffer] every S product that reads it is complete
