@@ -18,9 +18,10 @@
 // the CTA that arrives last joins them in CTA order (a fixed order: results do
 // not depend on which one that is).
 //
-// One producer warp walks the run: per piece (a unit's part in this CTA) it
-// puts the rows' bounds and Q into shared memory, then keeps the stages' TMA
-// copies in flight.  K rows land with the 128-byte swizzle, 4- and 5-bit V rows
+// A planning warp walks the run some pieces ahead (a piece is a unit's part in
+// this CTA): it puts each one's stages, first page numbers, row bounds and Q
+// into shared memory.  A loading warp keeps the stages' TMA copies in flight
+// across the pieces' borders.  K rows land with the 128-byte swizzle, 4- and 5-bit V rows
 // with the 64-byte swizzle, so that ldmatrix reads eight rows without bank
 // conflicts.  Four consumer warps take 32 keys of each stage, with a softmax
 // state of their own, and join at the piece's end.
@@ -52,7 +53,7 @@ namespace kvs {
 namespace {
 
 constexpr int kConsumers = 4;
-constexpr int kThreads = (kConsumers + 1) * 32;
+constexpr int kThreads = (kConsumers + 2) * 32;
 constexpr int kStageKeys = 128;
 constexpr int kLeastStages = 1;                    // a CTA's run
 constexpr int kQRow = 288;                         // bytes of a Q row in shared memory: 32 mod 128, so that 4 rows x 32 B are distinct banks
@@ -70,6 +71,7 @@ struct Piece {
     int slot;                 // record slot, or -1: the whole unit is here
     int cta0, n_ctas;         // CTAs that share the unit
     volatile int bad;         // a page number was outside the pool
+    int pages[32];            // the first pages, from first_stage / 2 on
     int token[ROWS], head[ROWS];
     int pos[ROWS], first[ROWS], end[ROWS];  // in keys of this phase
     float scale[ROWS], slope[ROWS];
@@ -86,13 +88,14 @@ struct Geo {
     static constexpr int kOffVd = kOffVh + kStageKeys * PG::kVhRow;
     static constexpr int kOffVm = kOffVd + kStageKeys * PG::kVdRow;
     static constexpr int kBytes = kOffVm + kStageKeys * PG::kVmRow;
-    static constexpr size_t kFixed = 1024 + kRedBytes + 2 * sizeof(Piece<kRows>) + 512;
+    static constexpr int kSlots = NT == 1 ? 4 : 3;                // pieces planned ahead
+    static constexpr size_t kFixed = 1024 + kRedBytes + kSlots * sizeof(Piece<kRows>) + 512;
     static constexpr int kPerSm = 2 * (2 * (size_t)kBytes + kFixed + 1024) <= 233472 ? 2 : 1;
     static constexpr int kFit = (int)((233472 / kPerSm - 1024 - kFixed) / kBytes);
     static constexpr int kStages = kFit < 4 ? kFit : 4;
     static constexpr size_t kOffRed = (size_t)kStages * kBytes;
     static constexpr size_t kOffPiece = kOffRed + kRedBytes;
-    static constexpr size_t kOffBar = kOffPiece + 2 * sizeof(Piece<kRows>);
+    static constexpr size_t kOffBar = kOffPiece + kSlots * sizeof(Piece<kRows>);
     static constexpr size_t kSmem = 1024 + kOffBar + 512;
     static_assert(kBytes % 1024 == 0 && kOffV % 1024 == 0, "swizzled tiles need aligned stages");
     static_assert(kStages >= 2 && kSmem <= 232448 && sizeof(Piece<kRows>) % 16 == 0, "shared memory");
@@ -192,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
     attend_few_kernel(const __grid_constant__ AttendPagesArgs a, const __grid_constant__ PageMaps maps) {
     using G = Geo<VT, KT, NT>;
     using PG = PageGeom<VT, KT>;
-    constexpr int ROWS = G::kRows, kStages = G::kStages;
+    constexpr int ROWS = G::kRows, kStages = G::kStages, kSlots = G::kSlots;
     extern __shared__ uint8_t smem_raw[];
     // aligned by an offset, not through an integer: a pointer made from an integer is
     // a generic one, and every access to it a generic load or store
@@ -201,10 +204,11 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
     Piece<ROWS>* pieces = reinterpret_cast<Piece<ROWS>*>(smem + G::kOffPiece);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::kOffBar);  // [stage] bytes landed
     uint64_t* empty = full + kStages;                                 // [stage] consumers done
-    uint64_t* p_full = empty + kStages;                               // [piece slot] published
-    uint64_t* p_empty = p_full + 2;                                   // [piece slot] consumers done
-    int* sLast = reinterpret_cast<int*>(p_empty + 2);                 // this CTA joins the unit
-    float* sml = reinterpret_cast<float*>(p_empty + 4);               // [warp][8][2] (reference, sum)
+    uint64_t* p_meta = empty + kStages;                               // [piece slot] stages and pages are there
+    uint64_t* p_full = p_meta + kSlots;                               // [piece slot] rows and Q too
+    uint64_t* p_empty = p_full + kSlots;                              // [piece slot] consumers and loader done
+    int* sLast = reinterpret_cast<int*>(p_empty + kSlots);            // this CTA joins the unit
+    float* sml = reinterpret_cast<float*>(p_empty + kSlots + 2);      // [warp][8][2] (reference, sum)
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n_kv = a.pool.n_kv;
@@ -215,16 +219,17 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], kConsumers);
         }
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(&p_meta[s], 1);
             mbar_init(&p_full[s], 1);
-            mbar_init(&p_empty[s], kConsumers);
+            mbar_init(&p_empty[s], kConsumers + 1);
         }
         fence_mbar_init();
     }
     __syncthreads();
 
     if (warp == kConsumers) {
-        // ============================ producer ============================
+        // ============================ planner ============================
         // ---- this CTA's run of the list of all units' stages: the sequences' shares,
         // 32 at a time, summed once for the whole and once up to the run's start ----
         auto share = [&](int i) -> long long {
@@ -260,7 +265,8 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
             base = __shfl_sync(0xffffffffu, upto, 31);
         }
         long long cur = run0;
-        int issued = 0, n_pieces = 0;
+        int slot = 0;
+        uint32_t slot_phase = 1;  // an unused slot's barrier counts as complete in phase 1
         bool ok = true;
         Seq s = seq < n_seqs ? seq_of<ROWS>(a, seq) : Seq{};
         while (ok) {
@@ -269,12 +275,15 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                 ++seq;
                 if (seq < n_seqs) s = seq_of<ROWS>(a, seq);
             }
-            Piece<ROWS>& p = pieces[n_pieces & 1];
-            if (n_pieces >= 2) ok = wait_phase(&p_empty[n_pieces & 1], ((n_pieces >> 1) - 1) & 1, a.batch.status);
+            Piece<ROWS>& p = pieces[slot];
+            ok = __all_sync(0xffffffffu, wait_phase(&p_empty[slot], slot_phase, a.batch.status));
             if (!ok || cur >= run1 || seq >= n_seqs) {
                 if (lane == 0) p.n_stages = -1;
                 __syncwarp();
-                if (lane == 0) arrive(&p_full[n_pieces & 1]);
+                if (lane == 0) {
+                    arrive(&p_meta[slot]);
+                    arrive(&p_full[slot]);
+                }
                 break;
             }
             const long long unit = quot(cur - base, s.n_stages);
@@ -339,62 +348,13 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                 // a row that may see keys beyond the page table
                 p.bad = hi > (long long)a.batch.table_stride * kPageTokens && !a.prefix_phase;
             }
-            // ---- the piece's stages: 128 keys each ----
+            // the first pages' numbers
             const int* table = a.prefix_phase ? a.prefix_table : a.batch.table + (size_t)seq * a.batch.table_stride;
             const int n_table = a.prefix_phase ? (a.prefix_len + kPageTokens - 1) / kPageTokens : a.batch.table_stride;
-            int pages = 0, pages_at = -1;  // 32 page numbers, one a lane
-            auto issue = [&](int st) -> bool {
-                const int j = st >> 1;
-                if (pages_at < 0 || j >= pages_at + 32) {
-                    pages_at = j;
-                    pages = j + lane < n_table ? table[j + lane] : -1;
-                }
-                int page = __shfl_sync(0xffffffffu, pages, j - pages_at);
-                const int buf = issued % kStages;
-                if (issued >= kStages &&
-                    !wait_phase(&empty[buf], ((issued / kStages) - 1) & 1, a.batch.status))
-                    return false;
-                if (lane == 0) {
-                    if ((unsigned)page >= (unsigned)a.pool.n_pages) {
-                        page = 0;  // some page: its piece comes out as NaN
-                        p.bad = 1;
-                    }
-                    uint8_t* dst = smem + buf * G::kBytes;
-                    uint64_t* bar = &full[buf];
-                    mbar_expect_tx(bar, G::kBytes);
-                    const int hp = page * a.pool.n_kv + h, t0 = (st & 1) * kStageKeys;
-                    const uint8_t* ph = a.pool.pages + (size_t)hp * PG::kHeadBytes;
-                    if constexpr (KT == kKF16) {
-                        tma4(dst, &maps.k, 0, 0, t0, hp, bar);
-                        tma4(dst + kStageKeys * 128, &maps.k, 0, 1, t0, hp, bar);
-                    } else {
-                        tma3(dst, &maps.k, 0, t0, hp, bar);
-                        bulk_load(dst + G::kOffKd, ph + PG::kOffKd + t0 * PG::kKdRow, kStageKeys * PG::kKdRow, bar);
-                    }
-                    if constexpr (VT == kVF16) {
-                        tma4(dst + G::kOffV, &maps.v, 0, 0, PG::kOffVq / 256 + t0, hp, bar);
-                        tma4(dst + G::kOffV + kStageKeys * 128, &maps.v, 0, 1, PG::kOffVq / 256 + t0, hp, bar);
-                    } else {
-                        tma3(dst + G::kOffV, &maps.v, 0, PG::kOffVq / PG::kVqRow + t0, hp, bar);
-                        bulk_load(dst + G::kOffVd, ph + PG::kOffVd + t0 * PG::kVdRow, kStageKeys * PG::kVdRow, bar);
-                    }
-                    if constexpr (PG::kVhRow > 0)
-                        bulk_load(dst + G::kOffVh, ph + PG::kOffVh + t0 * PG::kVhRow, kStageKeys * PG::kVhRow, bar);
-                    if constexpr (PG::kVmRow > 0)
-                        bulk_load(dst + G::kOffVm, ph + PG::kOffVm + t0 * PG::kVmRow, kStageKeys * PG::kVmRow, bar);
-                }
-                __syncwarp();
-                ++issued;
-                return true;
-            };
-            // the first stages' copies start before Q, which takes a while itself; they
-            // wait for no buffer but one that the piece before is done with
-            int st = st0;
-            for (; st < st1 && st < st0 + kStages; ++st) {
-                const bool free = issued < kStages || mbar_try_wait(&empty[issued % kStages], ((issued / kStages) - 1) & 1);
-                if (!__all_sync(0xffffffffu, free)) break;
-                issue(st);
-            }
+            const int j = (st0 >> 1) + lane;
+            p.pages[lane] = 2 * j < st1 && j < n_table ? table[j] : -1;
+            __syncwarp();
+            if (lane == 0) arrive(&p_meta[slot]);
             if (lane == 0) {
                 // the record slot, and the CTAs that share the unit
                 p.slot = (unit0 >= run0 && unit1 <= run1) ? -1 : (unit0 < run0 ? 0 : 1);
@@ -429,15 +389,85 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                 if (lane == 0) p.scale[r] = sc;
             }
             __syncwarp();
-            if (lane == 0) arrive(&p_full[n_pieces & 1]);
-
-            for (; ok && st < st1; ++st) ok = __all_sync(0xffffffffu, issue(st));
+            if (lane == 0) arrive(&p_full[slot]);
             cur = stop;
-            ++n_pieces;
+            if (++slot == kSlots) {
+                slot = 0;
+                slot_phase ^= 1;
+            }
+        }
+        return;
+    }
+
+    if (warp == kConsumers + 1) {
+        // ============================ loader ============================
+        int slot = 0, buf = 0;
+        uint32_t slot_phase = 0, buf_phase = 1;
+        long long issued = 0;
+        bool ok = true;
+        for (;;) {
+            ok = __all_sync(0xffffffffu, wait_phase(&p_meta[slot], slot_phase, a.batch.status));
+            Piece<ROWS>& p = pieces[slot];
+            if (!ok || p.n_stages < 0) break;
+            const int st0 = p.first_stage, st1 = st0 + p.n_stages, h = p.kv_head;
+            const int* table = a.prefix_phase ? a.prefix_table : a.batch.table + (size_t)p.seq * a.batch.table_stride;
+            const int n_table = a.prefix_phase ? (a.prefix_len + kPageTokens - 1) / kPageTokens : a.batch.table_stride;
+            int pages = p.pages[lane], pages_at = st0 >> 1;  // 32 page numbers, one a lane
+            for (int st = st0; st < st1; ++st) {
+                const int j = st >> 1;
+                if (j >= pages_at + 32) {
+                    pages_at = j;
+                    pages = j + lane < n_table ? table[j + lane] : -1;
+                }
+                int page = __shfl_sync(0xffffffffu, pages, j - pages_at);
+                ok = __all_sync(0xffffffffu, wait_phase(&empty[buf], buf_phase, a.batch.status));
+                if (!ok) break;
+                if (lane == 0) {
+                    if ((unsigned)page >= (unsigned)a.pool.n_pages) {
+                        page = 0;  // some page: its piece comes out as NaN
+                        p.bad = 1;
+                    }
+                    uint8_t* dst = smem + buf * G::kBytes;
+                    uint64_t* bar = &full[buf];
+                    mbar_expect_tx(bar, G::kBytes);
+                    const int hp = page * a.pool.n_kv + h, t0 = (st & 1) * kStageKeys;
+                    const uint8_t* ph = a.pool.pages + (size_t)hp * PG::kHeadBytes;
+                    if constexpr (KT == kKF16) {
+                        tma4(dst, &maps.k, 0, 0, t0, hp, bar);
+                        tma4(dst + kStageKeys * 128, &maps.k, 0, 1, t0, hp, bar);
+                    } else {
+                        tma3(dst, &maps.k, 0, t0, hp, bar);
+                        bulk_load(dst + G::kOffKd, ph + PG::kOffKd + t0 * PG::kKdRow, kStageKeys * PG::kKdRow, bar);
+                    }
+                    if constexpr (VT == kVF16) {
+                        tma4(dst + G::kOffV, &maps.v, 0, 0, PG::kOffVq / 256 + t0, hp, bar);
+                        tma4(dst + G::kOffV + kStageKeys * 128, &maps.v, 0, 1, PG::kOffVq / 256 + t0, hp, bar);
+                    } else {
+                        tma3(dst + G::kOffV, &maps.v, 0, PG::kOffVq / PG::kVqRow + t0, hp, bar);
+                        bulk_load(dst + G::kOffVd, ph + PG::kOffVd + t0 * PG::kVdRow, kStageKeys * PG::kVdRow, bar);
+                    }
+                    if constexpr (PG::kVhRow > 0)
+                        bulk_load(dst + G::kOffVh, ph + PG::kOffVh + t0 * PG::kVhRow, kStageKeys * PG::kVhRow, bar);
+                    if constexpr (PG::kVmRow > 0)
+                        bulk_load(dst + G::kOffVm, ph + PG::kOffVm + t0 * PG::kVmRow, kStageKeys * PG::kVmRow, bar);
+                }
+                __syncwarp();
+                ++issued;
+                if (++buf == kStages) {
+                    buf = 0;
+                    buf_phase ^= 1;
+                }
+            }
+            if (!ok) break;
+            if (lane == 0) arrive(&p_empty[slot]);
+            if (++slot == kSlots) {
+                slot = 0;
+                slot_phase ^= 1;
+            }
         }
         // a wait gave up: the copies in flight land before the memory is given back
-        for (int k = max(0, issued - kStages); !ok && k < issued; ++k)
-            wait_phase(&full[k % kStages], (k / kStages) & 1, a.batch.status);
+        for (long long k = max(0ll, issued - kStages); !ok && k < issued; ++k)
+            mbar_wait_bounded(&full[k % kStages], (k / kStages) & 1, a.batch.status);
         return;
     }
 
@@ -459,9 +489,11 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
             : "memory");
         return lost == 0;
     };
-    for (int n = 0;; ++n) {
-        Piece<ROWS>& p = pieces[n & 1];
-        ok = wait_phase(&p_full[n & 1], (n >> 1) & 1, a.batch.status);
+    int slot = 0;
+    uint32_t slot_phase = 0;
+    for (;;) {
+        Piece<ROWS>& p = pieces[slot];
+        ok = wait_phase(&p_full[slot], slot_phase, a.batch.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok || p.n_stages < 0) {
             consumers_sync();
@@ -933,7 +965,11 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
             }
         }
         if (!consumers_sync()) return;  // sLast and the join buffer are free again
-        if (lane == 0) arrive(&p_empty[n & 1]);
+        if (lane == 0) arrive(&p_empty[slot]);
+        if (++slot == kSlots) {
+            slot = 0;
+            slot_phase ^= 1;
+        }
     }
 }
 

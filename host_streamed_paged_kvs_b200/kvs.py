@@ -372,7 +372,15 @@ KVS_ERR_BAD_PAGE = 2
 # The make_* functions describe buffers once; the descriptors keep the tensors
 # alive and can be used for any number of calls, captured ones too.
 
-_DTYPES = {"torch.float16": KVS_DT_F16, "torch.bfloat16": KVS_DT_BF16, "torch.float32": KVS_DT_F32}
+_DTYPE_NAMES = {"torch.float16": KVS_DT_F16, "torch.bfloat16": KVS_DT_BF16, "torch.float32": KVS_DT_F32}
+_dtype_codes = {}  # dtype objects seen, by identity of the type itself
+
+
+def _dtype(x) -> Optional[int]:
+    try:
+        return _dtype_codes[x.dtype]
+    except KeyError:
+        return _dtype_codes.setdefault(x.dtype, _DTYPE_NAMES.get(str(x.dtype)))
 
 
 def _bad(msg: str):
@@ -446,13 +454,13 @@ def make_page_prefix(page_table, n_tokens: int) -> kvs_page_prefix:
 
 def _rows(x, batch, heads: int, what: str):
     """(descriptor, dtype code) of a [rows, heads, 128] device tensor, strides as they are."""
-    dt = _DTYPES.get(str(x.dtype))
-    shape = x.shape
+    dt = _dtype(x)
+    shape, stride = x.shape, x.stride()
     if dt is None or len(shape) != 3 or shape[0] < batch.n_rows or shape[1] != heads or shape[2] != 128 or \
-            (x.stride(2) != 1) or not x.is_cuda:
+            stride[2] != 1 or not x.is_cuda:
         _bad(f"{what}: a float16, bfloat16 or float32 device tensor [rows >= {batch.n_rows}, {heads}, 128] with "
              "contiguous heads is wanted")
-    return kvs_page_rows(x.data_ptr(), x.stride(0), x.stride(1)), dt
+    return kvs_page_rows(x.data_ptr(), stride[0], stride[1]), dt
 
 
 def _same(a: int, b: int, what: str) -> int:
@@ -505,7 +513,7 @@ def kvs_attend_pages(pool, batch, q, out, lse=None, score=None, prefix=None, wor
     (qr, dq), (orow, do) = _rows(q, batch, heads, "q"), _rows(out, batch, heads, "out")
     if workspace is None:
         _bad("a workspace is wanted (kvs_attend_pages_workspace bytes, zero-filled)")
-    if lse is not None and (str(lse.dtype) != "torch.float32" or not lse.is_contiguous() or lse.numel() < batch.n_rows * heads):
+    if lse is not None and (_dtype(lse) != KVS_DT_F32 or not lse.is_contiguous() or lse.numel() < batch.n_rows * heads):
         _bad("lse: a contiguous float32 tensor [n_rows, heads] is wanted")
     if score is not None:
         slopes, first, end = score.keep
