@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
         };
         const long long mine = share(lane);  // of the first 32, which are all of most batches
         long long total = mine;
+#pragma unroll 4
         for (int i = 32 + lane; i < n_seqs; i += 32) total += share(i);
 #pragma unroll
         for (int off = 16; off; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
@@ -364,29 +365,44 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
             // Q: fp16 as it is; bf16 as fp16 after taking each row's power of two
             // out (exact down to 2^-24 of the row's largest value)
             const float unit_scale = a.softcap > 0.0f || a.slopes ? a.scale : a.scale * 1.4426950408889634f;
-#pragma unroll 8
-            for (int r = 0; r < ROWS; ++r) {
-                const int tk = __shfl_sync(0xffffffffu, token, r), hd = __shfl_sync(0xffffffffu, head, r);
-                uint2 w = make_uint2(0u, 0u);
-                if (tk >= 0)
-                    w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q.p) + tk * a.q.row + hd * a.q.head + 4 * lane);
-                float sc = unit_scale;
-                if (a.q_dtype == kDtBF16) {
-                    const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
-                    const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
-                    float top = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y)));
+#pragma unroll 1
+            for (int r0 = 0; r0 < ROWS; r0 += 8) {
+                uint2 w[8];  // eight rows on their way at once
 #pragma unroll
-                    for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                    // 2^e with 2^e <= top < 2^(e+1); 1 for zero, subnormal and non-finite rows
-                    const uint32_t ex = (__float_as_uint(top) >> 23) & 0xffu;
-                    const bool plain = ex < 2 || ex > 252;
-                    const float up = plain ? 1.0f : __uint_as_float(ex << 23), down = plain ? 1.0f : __uint_as_float((254u - ex) << 23);
-                    *reinterpret_cast<__half2*>(&w.x) = __floats2half2_rn(x.x * down, x.y * down);
-                    *reinterpret_cast<__half2*>(&w.y) = __floats2half2_rn(y.x * down, y.y * down);
-                    sc *= up;
+                for (int k = 0; k < 8; ++k) {
+                    const int tk = __shfl_sync(0xffffffffu, token, r0 + k), hd = __shfl_sync(0xffffffffu, head, r0 + k);
+                    w[k] = make_uint2(0u, 0u);
+                    if (tk >= 0)
+                        w[k] = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q.p) + tk * a.q.row + hd * a.q.head + 4 * lane);
                 }
-                *reinterpret_cast<uint2*>(p.q + r * kQRow + 8 * lane) = w;
-                if (lane == 0) p.scale[r] = sc;
+                float up[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) up[k] = 1.0f;
+                if (a.q_dtype == kDtBF16) {
+                    uint32_t top[8];  // the largest magnitude's bits
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        top[k] = max(max(w[k].x & 0x7fffu, (w[k].x >> 16) & 0x7fffu), max(w[k].y & 0x7fffu, (w[k].y >> 16) & 0x7fffu));
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) top[k] = __reduce_max_sync(0xffffffffu, top[k]);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        // 2^e with 2^e <= top < 2^(e+1); 1 for zero, subnormal and non-finite rows
+                        const uint32_t ex = top[k] >> 7;
+                        const bool plain = ex < 2 || ex > 252;
+                        const float down = plain ? 1.0f : __uint_as_float((254u - ex) << 23);
+                        if (!plain) up[k] = __uint_as_float(ex << 23);
+                        *reinterpret_cast<__half2*>(&w[k].x) =
+                            __floats2half2_rn(__uint_as_float(w[k].x << 16) * down, __uint_as_float(w[k].x & 0xffff0000u) * down);
+                        *reinterpret_cast<__half2*>(&w[k].y) =
+                            __floats2half2_rn(__uint_as_float(w[k].y << 16) * down, __uint_as_float(w[k].y & 0xffff0000u) * down);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    *reinterpret_cast<uint2*>(p.q + (r0 + k) * kQRow + 8 * lane) = w[k];
+                    if (lane == 0) p.scale[r0 + k] = unit_scale * up[k];
+                }
             }
             __syncwarp();
             if (lane == 0) arrive(&p_full[slot]);

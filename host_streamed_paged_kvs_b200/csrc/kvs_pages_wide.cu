@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(kPlanThreads) wide_plan_kernel(const __grid_co
             if (n_groups + g >= max_groups) break;  // a malformed batch whose ranges overlap
             int ft, tk, keys;
             phase_seq(a, i0 + lo, ft, tk, keys);
+            const int tk_all = a.prefix_phase ? tk : a.batch.q_start[i0 + lo + 1] - ft;
             const int before = lo > 0 ? sUpto[lo - 1] : 0;
             WideUnit u;
             u.seq = i0 + lo;
@@ -232,6 +233,12 @@ __global__ void __launch_bounds__(kPlanThreads) wide_plan_kernel(const __grid_co
             const int t0 = ft + u.row0 / a.group, t1 = ft + (u.row0 + u.rows - 1) / a.group;
             const int shift = a.prefix_phase ? 0 : a.prefix_len;
             int from = INT_MAX, to = 0;
+            if (!a.first_key && !a.end_key && a.window <= 0) {
+                // causal only: the last row sees the most; the prefix is taken whole
+                from = 0;
+                to = keys;
+                if (!a.prefix_phase) to = min(keys, max(0, a.batch.seq_len[u.seq] - (ft + tk_all - 1 - t1)));
+            } else
             for (int t = t0 + lane; t <= t1; t += 32) {
                 if ((unsigned)t >= (unsigned)a.batch.n_rows) continue;
                 const int of = a.prefix_phase ? find_seq_thread(a.batch, t) : u.seq;
@@ -432,35 +439,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Q: fp16 as it is; bf16 with the row's power of two taken out
                 const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q.p) + (long long)max(token, 0) * a.q.row +
                                                                   (long long)head * a.q.head);
-                float up = 1.0f;
-                uint32_t top = 0;
-                if (a.q_dtype == kDtBF16 && token >= 0) {
-#pragma unroll 4
-                    for (int c = 0; c < 16; ++c) {
-                        const uint4 v = src[c];
-                        // the larger magnitude of two bf16, compared as integers
-                        top = max(top, max(max(v.x & 0x7fffu, (v.x >> 16) & 0x7fffu), max(v.y & 0x7fffu, (v.y >> 16) & 0x7fffu)));
-                        top = max(top, max(max(v.z & 0x7fffu, (v.z >> 16) & 0x7fffu), max(v.w & 0x7fffu, (v.w >> 16) & 0x7fffu)));
-                    }
-                }
-                const uint32_t ex = top >> 7;
-                const bool plain = ex < 2 || ex > 252;  // zero, subnormal and non-finite rows
-                // a negative scale turns Q, so that the largest product is the largest score
-                const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
-                const float down = plain ? sign : sign * __uint_as_float((254u - ex) << 23);
-                if (!plain) up = __uint_as_float(ex << 23);
-#pragma unroll 4
-                for (int c = 0; c < 16; ++c) {
-                    uint4 v = token >= 0 ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-                    if (a.q_dtype == kDtBF16) {
-                        uint32_t* x = &v.x;
+                uint4 v[16];  // the whole row on its way at once
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            x[i] = h2u(__floats2half2_rn(__uint_as_float(x[i] << 16) * down, __uint_as_float(x[i] & 0xffff0000u) * down));
-                    } else if (a.scale < 0.0f) {
-                        v = make_uint4(v.x ^ 0x80008000u, v.y ^ 0x80008000u, v.z ^ 0x80008000u, v.w ^ 0x80008000u);
+                for (int c = 0; c < 16; ++c) v[c] = token >= 0 ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+                float up = 1.0f;
+                // a negative scale turns Q, so that the largest product is the largest score
+                if (a.q_dtype == kDtBF16) {
+                    uint32_t top = 0;  // the largest magnitude's bits
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const uint32_t x[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) top = max(top, max(x[i] & 0x7fffu, (x[i] >> 16) & 0x7fffu));
                     }
-                    st_chunk(sq, trow, c, v);
+                    const uint32_t ex = top >> 7;
+                    const bool plain = ex < 2 || ex > 252;  // zero, subnormal and non-finite rows
+                    const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
+                    const float down = plain ? sign : sign * __uint_as_float((254u - ex) << 23);
+                    if (!plain) up = __uint_as_float(ex << 23);
+                    auto two = [&](uint32_t x) {
+                        return h2u(__floats2half2_rn(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xffff0000u) * down));
+                    };
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) st_chunk(sq, trow, c, make_uint4(two(v[c].x), two(v[c].y), two(v[c].z), two(v[c].w)));
+                } else {
+                    const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) st_chunk(sq, trow, c, make_uint4(v[c].x ^ sign, v[c].y ^ sign, v[c].z ^ sign, v[c].w ^ sign));
                 }
                 sc = fabsf(formed ? a.scale : a.scale * 1.4426950408889634f) * up;
             }
@@ -496,14 +501,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c0 = 0; c0 < kStageKeys; c0 += 32) {
                         float s[32];
                         tmem_ld32(t_s + c0, s);
-                        if (formed) {
+                        if (a.softcap > 0.0f) {
+                            const float in = sc * a.inv_cap * 2.8853900817779268f, cap = a.softcap * 1.4426950408889634f;
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) s[c] = score_log2(a, s[c] * sc, slope, pos, key0 + c0 + c);
+                            for (int c = 0; c < 32; ++c)  // cap tanh(x): cap - 2 cap / (e^2x + 1)
+                                s[c] = fmaf(-2.0f * cap, __fdividef(1.0f, exp2_fast(s[c] * in) + 1.0f), cap);
                         }
-                        const int f = first - key0 - c0, e = end - key0 - c0;
+                        if (a.slopes) {
+                            const float k = slope * -1.4426950408889634f, m = a.softcap > 0.0f ? 1.0f : sc * 1.4426950408889634f;
+                            const float d = (float)(pos - key0 - c0);
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (c < f || c >= e) s[c] = -CUDART_INF_F;
+                            for (int c = 0; c < 32; ++c) s[c] = fmaf(fabsf(d - (float)c), k, s[c] * m);
+                        }
+                        if (masked) {
+                            const int f = min(max(first - key0 - c0, 0), 32), e = min(max(end - key0 - c0, 0), 32);
+                            const uint32_t seen = e > f ? (0xffffffffu >> (32 - e + f)) << f : 0u;  // bits f .. e - 1
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (!((seen >> c) & 1u)) s[c] = -CUDART_INF_F;
+                        }
                         tmem_st32(t_s + c0, s);
                     }
                 }
@@ -960,22 +976,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32) wide_join_kernel(const __grid
     for (int r = blockIdx.y * kJoinWarps + warp; r < w.u.rows; r += gridDim.y * kJoinWarps) {
         const int fr = w.u.row0 + r, token = ft + fr / a.group, head = w.h * a.group + fr % a.group;
         if ((unsigned)token >= (unsigned)a.batch.n_rows || (a.prefix_phase && find_seq_thread(a.batch, token) < 0)) continue;
-        auto record = [&](int c) { return a.records + ((size_t)(c * 2 + (c == c0 ? 1 : 0)) * kWideRows + r) * kRecordFloats; };
         float M = -CUDART_INF_F, L = 0.0f;
-        for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, record(c)[128]);
-#pragma unroll
-        for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) {
-            const float4 v = reinterpret_cast<const float4*>(record(c))[lane];
-            const float2 ml = *reinterpret_cast<const float2*>(record(c) + 128);
-            const float f = ml.x == M ? 1.0f : exp2_fast(ml.x - M);
-            acc.x = fmaf(v.x, f, acc.x);
-            acc.y = fmaf(v.y, f, acc.y);
-            acc.z = fmaf(v.z, f, acc.z);
-            acc.w = fmaf(v.w, f, acc.w);
-            L = fmaf(ml.y, f, L);
+        constexpr int kBatch = 8;  // records on their way at once
+#pragma unroll 1
+        for (int c = c0; c <= c1; c += kBatch) {
+            float4 v[kBatch];
+            float2 ml[kBatch];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const float* rec = a.records + ((size_t)(min(c + b, c1) * 2 + (c + b == c0 ? 1 : 0)) * kWideRows + r) * kRecordFloats;
+                v[b] = reinterpret_cast<const float4*>(rec)[lane];
+                ml[b] = *reinterpret_cast<const float2*>(rec + 128);
+            }
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+                if (c + b <= c1) join(acc, M, L, v[b], ml[b].x, ml[b].y);
         }
         finish_row<VT, KT>(a, w.u.seq, token, head, acc, M, L);
     }
@@ -995,7 +1011,7 @@ cudaError_t launch(const AttendPagesArgs& a, const PageMaps& maps, int n_sms, cu
     const long long groups = wide_groups(a.batch.n_rows, a.group, a.prefix_phase ? 1 : a.batch.n_seqs);
     wide_plan_kernel<<<1, kPlanThreads, 0, s>>>(a, (int)std::min(groups, 0x7fffffffll));
     attend_wide_kernel<VT, KT><<<ctas, kThreads, kSmem, s>>>(a, maps);
-    if (ctas > 1) wide_join_kernel<VT, KT><<<dim3(ctas - 1, 8), kJoinWarps * 32, 0, s>>>(a, ctas);
+    if (ctas > 1) wide_join_kernel<VT, KT><<<dim3(ctas - 1, 16), kJoinWarps * 32, 0, s>>>(a, ctas);
     return cudaGetLastError();
 }
 
