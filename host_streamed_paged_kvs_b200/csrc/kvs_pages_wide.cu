@@ -18,15 +18,18 @@
 //     tensor memory 16 columns at a time; the weights 2^(s - r) with the row's
 //     kept reference are packed to fp16 and put back over S.  A row's maximum is
 //     taken only when its weights' sum says that the reference is too low (over
-//     2^13, or the first keys seen): then the row of O is rescaled.
+//     2^13, or the first keys seen): then the row of O is rescaled, once the
+//     product before is complete.  (One S of 128 keys a tile, its next only after
+//     the weights are taken: 460 us on a 256-token chunk at 64K; N = 128 products
+//     are faster, but scores, softmax and product then wait for each other.)
 //   warps 8..11 and 12..14: convert K and V of each stage to fp16 operand tiles
 //     (128-byte swizzle); the next stage's codes are on their way to registers
 //     meanwhile.  A warp converts one operand only: the fence that hands a tile to
 //     the tensor cores waits for the warp's loads in flight, so loads of the other
 //     operand would be waited for too (a 256-token chunk at 64K: 432 us).  fp16
 //     rows come by TMA instead, as they are.
-//   warp 15: one thread issues S = Q K^T and O += P V of the two tiles in turn,
-//     so that one tile's softmax runs under the other's products.
+//   warp 15: its elected lane issues S = Q K^T of both tiles a sub-stage ahead,
+//     and O += P V as the weights come.
 // K and V are rounded to fp16 once (d q), the weights once; sums and softmax
 // statistics are fp32.
 #include <cuda_bf16.h>
@@ -57,9 +60,10 @@ constexpr size_t kSmem = 1024 + kOffBar + 256;
 static_assert(kSmem <= 232448, "shared memory");
 constexpr float kSumMost = 8192.0f;                   // a row's weights of one stage: fp16 holds each
 constexpr uint32_t kColS = 0, kColO = 256;            // tensor memory columns, + 128 per tile
-// f16 x f16 -> f32, M = N = 128, A K-major (Q) or from tensor memory (P); B K-major (K), MN-major (V)
-constexpr uint32_t kIdescS = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-constexpr uint32_t kIdescPV = kIdescS | (1u << 16);
+constexpr int kSubKeys = 64;                          // keys of an S tile: two per stage
+// f16 x f16 -> f32, M = 128, A K-major (Q) or from tensor memory (P); S: N = 64 keys, B K-major; PV: N = 128 dims, B MN-major
+constexpr uint32_t kIdescS = (1u << 4) | ((64u >> 3) << 17) | ((128u >> 4) << 24);
+constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 
 // shared-memory matrix descriptor (version 1, 128-byte swizzle): rows of 128
 // bytes in groups of 8, 64-column halves 16 KB apart
@@ -130,22 +134,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     unsigned long long r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a.x, a.y)), "l"(f2_bits(b.x, b.y)));
     return make_float2(__uint_as_float((uint32_t)r), __uint_as_float((uint32_t)(r >> 32)));
-}
-// 16 columns of tensor memory on their way into registers; tmem_here makes them usable
-__device__ __forceinline__ void tmem_fetch(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_here(uint32_t (&r)[16]) {
-    // the wait names the registers, so no use of them is scheduled ahead of it
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
 }
 // 16 columns into tensor memory, without waiting for them
 __device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t* r) {
@@ -343,12 +331,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* v_full = bars + 4;
     uint64_t* v_free = bars + 6;
     uint64_t* v_raw = bars + 8;     // [buffer] fp16 V landed
-    uint64_t* s_full = bars + 10;   // [tile] S complete
-    uint64_t* p_full = bars + 12;   // [tile] weights written
-    uint64_t* o_full = bars + 14;   // [tile] the piece's last product complete
-    uint64_t* q_full = bars + 16;   // [tile] Q written
-    uint64_t* done = bars + 18;     // every product complete
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19);
+    uint64_t* s_full = bars + 10;   // [tile][half] S complete
+    uint64_t* p_full = bars + 14;   // [tile][half] weights written
+    uint64_t* o_done = bars + 18;   // [tile][half] the P V product complete (by half: a waiter is then never
+                                    // two phases behind, which would look like none)
+    uint64_t* q_full = bars + 22;   // [tile] Q written
+    uint64_t* done = bars + 24;     // every product complete
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 25);
     int* sGroup = reinterpret_cast<int*>(tmem_slot + 1);
     volatile int* sAbort = reinterpret_cast<volatile int*>(sGroup + 1);
 
@@ -366,10 +355,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&v_full[i], kVWarps);
             mbar_init(&v_free[i], 1);
             mbar_init(&v_raw[i], 1);
+            mbar_init(&q_full[i], 4);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&o_done[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
-            mbar_init(&o_full[i], 1);
-            mbar_init(&q_full[i], 4);
         }
         mbar_init(done, 1);
         fence_mbar_init();
@@ -406,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t t_s = tmem + lanes + kColS + tile * 128, t_o = tmem + lanes + kColO + tile * 128;
         uint8_t* sq = smem + kOffQ + tile * kTileBytes;
         const bool formed = a.softcap > 0.0f || a.slopes;
-        uint32_t n_s = 0, n_o = 0;  // S and O completions waited for
+        uint32_t n_sub = 0;  // sub-stages of this tile so far: S, P and O phases go by it
         for (long long cur = run0; cur < run1 && walk_to(a, w, cur, n_groups);) {
             const long long unit1 = w.unit0 + w.u.n_stages, stop = min(run1, unit1);
             const int n_st = (int)(stop - cur), st0 = w.u.stage0 + (int)(cur - w.unit0);
@@ -486,21 +477,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             // keys that every row of this warp sees
             const int all_from = __reduce_max_sync(0xffffffffu, token >= 0 ? first : 0);
             const int all_to = __reduce_min_sync(0xffffffffu, token >= 0 ? end : INT_MAX);
-            for (int i = 0; i < n_st; ++i) {
-                const int key0 = (st0 + i) * kStageKeys;
-                wait(&s_full[tile], n_s & 1);
+            for (int i = 0; i < 2 * n_st; ++i, ++n_sub) {
+                const int key0 = st0 * kStageKeys + i * kSubKeys;
+                const int hb = n_sub & 1;  // which of the tile's two S buffers
+                const uint32_t t_sub = t_s + 64 * hb;
+                wait(&s_full[2 * tile + hb], (n_sub >> 1) & 1);
                 if (!__all_sync(0xffffffffu, ok)) break;
-                ++n_s;
                 tc_fence_after();
-                const bool masked = key0 < all_from || key0 + kStageKeys > all_to;  // uniform
+                const bool masked = key0 < all_from || key0 + kSubKeys > all_to;  // uniform
                 if (formed || masked) {
                     // caps, distances and masks: the scores are formed in place first, so that
-                    // the two passes below stay short (unrolled code for every case outgrows the
-                    // instruction cache, which the other roles' loops share)
+                    // the pass below stays short
 #pragma unroll 1
-                    for (int c0 = 0; c0 < kStageKeys; c0 += 32) {
+                    for (int c0 = 0; c0 < kSubKeys; c0 += 32) {
                         float s[32];
-                        tmem_ld32(t_s + c0, s);
+                        tmem_ld32(t_sub + c0, s);
                         if (a.softcap > 0.0f) {
                             const float in = sc * a.inv_cap * 2.8853900817779268f, cap = a.softcap * 1.4426950408889634f;
 #pragma unroll
@@ -520,58 +511,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int c = 0; c < 32; ++c)
                                 if (!((seen >> c) & 1u)) s[c] = -CUDART_INF_F;
                         }
-                        tmem_st32(t_s + c0, s);
+                        tmem_st32(t_sub + c0, s);
                     }
                 }
                 const float mul = formed ? 1.0f : sc;
-                // ---- weights with the row's kept reference, 16 columns at a time, the next
-                // ones on their way; put back over the scores when the row's sum says that
-                // the reference stands ----
+                // ---- weights with the row's kept reference; put back over the scores when the
+                // row's sum says that the reference stands ----
                 const float2 mul2 = make_float2(mul, mul);
-                uint32_t p[64];
+                uint32_t p[32];
                 float sum;
 #pragma unroll 1
                 for (int round = 0;; ++round) {
                     const float mu = ref == -CUDART_INF_F ? 0.0f : -ref;
                     const float2 mu2 = make_float2(mu, mu);
                     float2 s0 = make_float2(0.0f, 0.0f), s1 = make_float2(0.0f, 0.0f);
-                    uint32_t r[2][16];
-                    tmem_fetch(t_s, r[0]);
+                    float x[64];
+                    tmem_ld64(t_sub, x);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        uint32_t(&x)[16] = r[k & 1];
-                        tmem_here(x);
-                        if (k < 7) tmem_fetch(t_s + 16 * (k + 1), r[(k + 1) & 1]);
-#pragma unroll
-                        for (int c = 0; c < 16; c += 4) {
-                            float2 u = fma2(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), mul2, mu2);
-                            float2 v = fma2(make_float2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), mul2, mu2);
-                            u = make_float2(exp2_fast(u.x), exp2_fast(u.y));
-                            v = make_float2(exp2_fast(v.x), exp2_fast(v.y));
-                            s0 = add2(s0, u);
-                            s1 = add2(s1, v);
-                            p[8 * k + c / 2] = h2u(__floats2half2_rn(u.x, u.y));
-                            p[8 * k + c / 2 + 1] = h2u(__floats2half2_rn(v.x, v.y));
-                        }
+                    for (int c = 0; c < 64; c += 4) {
+                        float2 u = fma2(make_float2(x[c], x[c + 1]), mul2, mu2);
+                        float2 v = fma2(make_float2(x[c + 2], x[c + 3]), mul2, mu2);
+                        u = make_float2(exp2_fast(u.x), exp2_fast(u.y));
+                        v = make_float2(exp2_fast(v.x), exp2_fast(v.y));
+                        s0 = add2(s0, u);
+                        s1 = add2(s1, v);
+                        p[c / 2] = h2u(__floats2half2_rn(u.x, u.y));
+                        p[c / 2 + 1] = h2u(__floats2half2_rn(v.x, v.y));
                     }
                     s0 = add2(s0, s1);
                     sum = s0.x + s0.y;
-                    const bool low = token >= 0 && (!(sum <= kSumMost) || (ref == -CUDART_INF_F && max(first, key0) < min(end, key0 + kStageKeys)));
+                    const bool low = token >= 0 && (!(sum <= kSumMost) || (ref == -CUDART_INF_F && max(first, key0) < min(end, key0 + kSubKeys)));
                     if (round || !__any_sync(0xffffffffu, low)) break;
                     // the row's maximum: the reference goes 4 below it, and O with it
                     float top = -CUDART_INF_F;
-#pragma unroll 1
-                    for (int c0 = 0; c0 < kStageKeys; c0 += 32) {
-                        float s[32];
-                        tmem_ld32(t_s + c0, s);
+                    tmem_ld64(t_sub, x);
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) top = fmaxf(top, s[c]);
-                    }
+                    for (int c = 0; c < 64; ++c) top = fmaxf(top, x[c]);
                     const float now = low ? fmaxf(ref, top * mul - 4.0f) : ref;
                     const float f = now == ref ? 1.0f : exp2_fast(ref - now);
                     ref = now;
                     l *= f;
-                    if (i > 0) {  // the product before this S is complete, and none is in flight for this tile
+                    if (i > 0) {
+                        // the product before must be complete; the next one needs this warp's weights
+                        wait(&o_done[2 * tile + (hb ^ 1)], ((n_sub - 1) >> 1) & 1);
+                        tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < 128; c += 32) {
                             float o[32];
@@ -582,17 +565,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
+                if (!__all_sync(0xffffffffu, ok)) break;
                 l += sum;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) tmem_put16(t_s + 16 * k, p + 16 * k);
+                tmem_put16(t_sub, p);
+                tmem_put16(t_sub + 16, p + 16);
                 tmem_put_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive(&p_full[tile]);
+                if (lane == 0) arrive(&p_full[2 * tile + hb]);
             }
-            wait(&o_full[tile], n_o & 1);
             if (!__all_sync(0xffffffffu, ok)) break;
-            ++n_o;
+            wait(&o_done[2 * tile + 1], ((n_sub - 1) >> 1) & 1);
+            if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
 
             // ---- the piece's end: O through shared memory (this warp's rows of Q), 64
@@ -895,51 +879,62 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n_st = (int)(stop - cur);
             const int tiles = w.u.rows > 128 ? 2 : 1;
             cur = stop;
-            auto scores = [&](int t, uint32_t kb) {
-                const uint32_t q = smem0 + kOffQ + t * kTileBytes, k = smem0 + kOffK + kb * kTileBytes;
+            // S of sub-stage j of tile t: 64 keys, half of the stage's K tile
+            auto scores = [&](int t, uint32_t kb, uint32_t sub) {
+                const uint32_t half = sub & 1;
+                const uint32_t q = smem0 + kOffQ + t * kTileBytes, k = smem0 + kOffK + kb * kTileBytes + half * (kSubKeys * 128);
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) mma_ss(tmem + kColS + 128 * t, desc_k(q, kk), desc_k(k, kk), kIdescS, kk > 0, one);
-                commit_one(&s_full[t], one);
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_ss(tmem + kColS + 128 * t + 64 * half, desc_k(q, kk), desc_k(k, kk), kIdescS, kk > 0, one);
+                commit_one(&s_full[2 * t + half], one);
             };
             wait(&k_full[n_k & 1], (n_k >> 1) & 1);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 if (t >= tiles) break;
                 wait(&q_full[t], n_q[t] & 1);
-                if (!__all_sync(0xffffffffu, ok)) break;
                 ++n_q[t];
+                if (!__all_sync(0xffffffffu, ok)) break;
                 tc_fence_after();
-                scores(t, n_k & 1);
+                scores(t, n_k & 1, 0);
             }
             if (!__all_sync(0xffffffffu, ok)) break;
-            commit_one(&k_free[n_k & 1], one);
-            ++n_k;
-            for (int i = 0; i < n_st; ++i) {
-                const uint32_t vb = n_v & 1;
-                wait(&v_full[vb], (n_v >> 1) & 1);
-                if (i + 1 < n_st) wait(&k_full[n_k & 1], (n_k >> 1) & 1);
+            for (int i = 0; i < 2 * n_st; ++i) {
+                // the next S of both tiles goes first: its buffer's weights were taken by
+                // the products of the sub-stage before this one, issued already
+                if (i + 1 < 2 * n_st) {
+                    if (((i + 1) & 1) == 0) wait(&k_full[n_k & 1], (n_k >> 1) & 1);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        if (t < tiles) scores(t, n_k & 1, i + 1);
+                    if ((i + 1) & 1) {  // the second half: K is read once these are complete
+                        commit_one(&k_free[n_k & 1], one);
+                        ++n_k;
+                    }
+                }
+                const uint32_t vb = n_v & 1, half = i & 1;
+                if (half == 0) wait(&v_full[vb], (n_v >> 1) & 1);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if (t >= tiles) break;
-                    wait(&p_full[t], n_p[t] & 1);
+                    wait(&p_full[2 * t + half], n_p[t] & 1);  // n_p: stages of this tile
+                    if (half == 1) ++n_p[t];
                     if (!__all_sync(0xffffffffu, ok)) break;
-                    ++n_p[t];
                     tc_fence_after();
                     const uint32_t v = smem0 + kOffV + vb * kTileBytes;
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * kk, desc_mn(v, kk), kIdescPV, i > 0 || kk > 0, one);
-                    if (t == tiles - 1) commit_one(&v_free[vb], one);
-                    if (i + 1 < n_st) {
-                        scores(t, n_k & 1);
-                        if (t == tiles - 1) commit_one(&k_free[n_k & 1], one);
-                    } else {
-                        commit_one(&o_full[t], one);
-                    }
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 64 * half + 8 * kk, desc_mn(v, 4 * half + kk), kIdescPV,
+                               i > 0 || kk > 0, one);
+                    commit_one(&o_done[2 * t + half], one);
                 }
                 if (!__all_sync(0xffffffffu, ok)) break;
-                if (i + 1 < n_st) ++n_k;
-                ++n_v;
+                if (half == 1) {
+                    commit_one(&v_free[vb], one);
+                    ++n_v;
+                }
             }
         }
         if (run0 < run1) {  // nothing is in flight when the memory is given back
