@@ -378,6 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     bool ok = run0 < run1;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {  // by one thread or a whole warp
+        if (ok && mbar_try_wait(bar, parity)) return true;
         if (!ok || *sAbort) return ok = false;
         if (!wait_phase(bar, parity, a.batch.status)) {
             ok = false;
@@ -525,18 +526,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float mu = ref == -CUDART_INF_F ? 0.0f : -ref;
                     const float2 mu2 = make_float2(mu, mu);
                     float2 s0 = make_float2(0.0f, 0.0f), s1 = make_float2(0.0f, 0.0f);
-                    float x[64];
-                    tmem_ld64(t_sub, x);
 #pragma unroll
-                    for (int c = 0; c < 64; c += 4) {
-                        float2 u = fma2(make_float2(x[c], x[c + 1]), mul2, mu2);
-                        float2 v = fma2(make_float2(x[c + 2], x[c + 3]), mul2, mu2);
-                        u = make_float2(exp2_fast(u.x), exp2_fast(u.y));
-                        v = make_float2(exp2_fast(v.x), exp2_fast(v.y));
-                        s0 = add2(s0, u);
-                        s1 = add2(s1, v);
-                        p[c / 2] = h2u(__floats2half2_rn(u.x, u.y));
-                        p[c / 2 + 1] = h2u(__floats2half2_rn(v.x, v.y));
+                    for (int c0 = 0; c0 < kSubKeys; c0 += 32) {  // 64 at once would not fit the registers
+                        float x[32];
+                        tmem_ld32(t_sub + c0, x);
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4) {
+                            float2 u = fma2(make_float2(x[c], x[c + 1]), mul2, mu2);
+                            float2 v = fma2(make_float2(x[c + 2], x[c + 3]), mul2, mu2);
+                            u = make_float2(exp2_fast(u.x), exp2_fast(u.y));
+                            v = make_float2(exp2_fast(v.x), exp2_fast(v.y));
+                            s0 = add2(s0, u);
+                            s1 = add2(s1, v);
+                            p[(c0 + c) / 2] = h2u(__floats2half2_rn(u.x, u.y));
+                            p[(c0 + c) / 2 + 1] = h2u(__floats2half2_rn(v.x, v.y));
+                        }
                     }
                     s0 = add2(s0, s1);
                     sum = s0.x + s0.y;
@@ -544,9 +548,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (round || !__any_sync(0xffffffffu, low)) break;
                     // the row's maximum: the reference goes 4 below it, and O with it
                     float top = -CUDART_INF_F;
-                    tmem_ld64(t_sub, x);
+#pragma unroll 1
+                    for (int c0 = 0; c0 < kSubKeys; c0 += 32) {
+                        float x[32];
+                        tmem_ld32(t_sub + c0, x);
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) top = fmaxf(top, x[c]);
+                        for (int c = 0; c < 32; ++c) top = fmaxf(top, x[c]);
+                    }
                     const float now = low ? fmaxf(ref, top * mul - 4.0f) : ref;
                     const float f = now == ref ? 1.0f : exp2_fast(ref - now);
                     ref = now;
@@ -745,10 +753,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int g = 0; g < kMine; ++g) {
                         const int row = 4 * (pw + kKWarps * g) + rl;
-                        uint4 lo, hi;
-                        conv_s8(kc[g], h2u(__half2half2(kd[g])), lo, hi);
-                        st_chunk(kt, row, 2 * ch, lo);
-                        st_chunk(kt, row, 2 * ch + 1, hi);
+                        if (pw + kKWarps * g < 32) {
+                            uint4 lo, hi;
+                            conv_s8(kc[g], h2u(__half2half2(kd[g])), lo, hi);
+                            st_chunk(kt, row, 2 * ch, lo);
+                            st_chunk(kt, row, 2 * ch + 1, hi);
+                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -872,69 +882,67 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ============================ products ============================
         const uint32_t one = elect_one();
+        // descriptors of the first operands; the others differ by constants (the address
+        // field counts 16 bytes, and 227 KB stay below its 14 bits)
         const uint32_t smem0 = smem_u32(smem);
+        const uint64_t dq = desc_k(smem0 + kOffQ, 0), dk = desc_k(smem0 + kOffK, 0), dv = desc_mn(smem0 + kOffV, 0);
         uint32_t n_k = 0, n_v = 0, n_p[2] = {0, 0}, n_q[2] = {0, 0};
         for (long long cur = run0; ok && cur < run1 && walk_to(a, w, cur, n_groups);) {
             const long long stop = min(run1, w.unit0 + w.u.n_stages);
             const int n_st = (int)(stop - cur);
             const int tiles = w.u.rows > 128 ? 2 : 1;
             cur = stop;
-            // S of sub-stage j of tile t: 64 keys, half of the stage's K tile
-            auto scores = [&](int t, uint32_t kb, uint32_t sub) {
-                const uint32_t half = sub & 1;
-                const uint32_t q = smem0 + kOffQ + t * kTileBytes, k = smem0 + kOffK + kb * kTileBytes + half * (kSubKeys * 128);
+            // S of a sub-stage of tile t: 64 keys, half of the stage's K tile
+            auto scores = [&](int t, uint32_t half) {
+                const uint64_t k = dk + ((n_k & 1) * kTileBytes + half * (kSubKeys * 128)) / 16;
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_ss(tmem + kColS + 128 * t + 64 * half, desc_k(q, kk), desc_k(k, kk), kIdescS, kk > 0, one);
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) / 16;
+                    mma_ss(tmem + kColS + 128 * t + 64 * half, dq + t * (kTileBytes / 16) + off, k + off, kIdescS, kk > 0, one);
+                }
                 commit_one(&s_full[2 * t + half], one);
             };
             wait(&k_full[n_k & 1], (n_k >> 1) & 1);
+            wait(&q_full[0], n_q[0]++ & 1);
+            if (tiles > 1) wait(&q_full[1], n_q[1]++ & 1);
+            if (!ok) break;
+            tc_fence_after();
+            scores(0, 0);
+            if (tiles > 1) scores(1, 0);
+#pragma unroll 1
+            for (int i = 0; i < n_st; ++i) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (t >= tiles) break;
-                wait(&q_full[t], n_q[t] & 1);
-                ++n_q[t];
-                if (!__all_sync(0xffffffffu, ok)) break;
-                tc_fence_after();
-                scores(t, n_k & 1, 0);
-            }
-            if (!__all_sync(0xffffffffu, ok)) break;
-            for (int i = 0; i < 2 * n_st; ++i) {
-                // the next S of both tiles goes first: its buffer's weights were taken by
-                // the products of the sub-stage before this one, issued already
-                if (i + 1 < 2 * n_st) {
-                    if (((i + 1) & 1) == 0) wait(&k_full[n_k & 1], (n_k >> 1) & 1);
-                    if (!__all_sync(0xffffffffu, ok)) break;
-                    tc_fence_after();
+                for (uint32_t half = 0; half < 2; ++half) {
+                    const bool next = half == 0 || i + 1 < n_st;
+                    if (half == 1 && next) wait(&k_full[n_k & 1], (n_k >> 1) & 1);
+                    if (half == 0) wait(&v_full[n_v & 1], (n_v >> 1) & 1);
+                    const uint64_t v = dv + ((n_v & 1) * kTileBytes + half * 4 * 2048) / 16;
+                    // a tile's next S goes before its product: the buffer's weights were taken
+                    // by the product before, issued already.  Tile by tile, so that the two
+                    // tiles' softmax warps do not all work at once
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        if (t < tiles) scores(t, n_k & 1, i + 1);
-                    if ((i + 1) & 1) {  // the second half: K is read once these are complete
+                    for (int t = 0; t < 2; ++t) {
+                        if (t >= tiles) break;
+                        tc_fence_after();
+                        if (next) scores(t, half ^ 1);
+                        wait(&p_full[2 * t + half], n_p[t] & 1);  // n_p: stages of this tile
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 64 * half + 8 * kk, v + kk * (2048 / 16), kIdescPV,
+                                   (half || kk) ? 1u : (i > 0), one);
+                        commit_one(&o_done[2 * t + half], one);
+                    }
+                    if (half == 0) {
                         commit_one(&k_free[n_k & 1], one);
                         ++n_k;
                     }
                 }
-                const uint32_t vb = n_v & 1, half = i & 1;
-                if (half == 0) wait(&v_full[vb], (n_v >> 1) & 1);
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (t >= tiles) break;
-                    wait(&p_full[2 * t + half], n_p[t] & 1);  // n_p: stages of this tile
-                    if (half == 1) ++n_p[t];
-                    if (!__all_sync(0xffffffffu, ok)) break;
-                    tc_fence_after();
-                    const uint32_t v = smem0 + kOffV + vb * kTileBytes;
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 64 * half + 8 * kk, desc_mn(v, 4 * half + kk), kIdescPV,
-                               i > 0 || kk > 0, one);
-                    commit_one(&o_done[2 * t + half], one);
-                }
-                if (!__all_sync(0xffffffffu, ok)) break;
-                if (half == 1) {
-                    commit_one(&v_free[vb], one);
-                    ++n_v;
-                }
+                if (!ok) break;
+                commit_one(&v_free[n_v & 1], one);
+                ++n_v;
+                ++n_p[0];
+                if (tiles > 1) ++n_p[1];
             }
         }
         if (run0 < run1) {  // nothing is in flight when the memory is given back
