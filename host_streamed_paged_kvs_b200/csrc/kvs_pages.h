@@ -88,11 +88,11 @@ struct WideUnit {
     int seq, row0, rows;     // rows row0 .. row0 + rows - 1 of the sequence, token-major
     int stage0, n_stages;    // at least 1
     int n_keys;              // keys that exist
-    long long before;        // stages of the groups before this one
+    long long before;        // length of the groups before this one in the list
 };
 struct WidePlan {
     int n_groups, pad;
-    long long total;         // stages of all groups
+    long long total;         // length of all groups in the list
 };
 constexpr int kWideRows = 256;
 constexpr int kWideCtas = 148;

@@ -123,9 +123,8 @@ __device__ __noinline__ float4 slow_row(const AttendPagesArgs& a, int seq, int r
     return make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
 }
 
-// four values of a row of the result
-__device__ __forceinline__ void store_out4(const AttendPagesArgs& a, int row, int head, int d, const float4& o) {
-    const long long to = row * a.out.row + head * a.out.head + d;
+// four values of the result
+__device__ __forceinline__ void store_out4_at(const AttendPagesArgs& a, long long to, const float4& o) {
     if (a.out_dtype == kDtF32) {
         *reinterpret_cast<float4*>(static_cast<float*>(a.out.p) + to) = o;
         return;
@@ -139,6 +138,10 @@ __device__ __forceinline__ void store_out4(const AttendPagesArgs& a, int row, in
         *reinterpret_cast<__nv_bfloat162*>(&w.y) = __floats2bfloat162_rn(o.z, o.w);
     }
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out.p) + to) = w;
+}
+
+__device__ __forceinline__ void store_out4(const AttendPagesArgs& a, int row, int head, int d, const float4& o) {
+    store_out4_at(a, row * a.out.row + head * a.out.head + d, o);
 }
 
 // (acc, M, L) += (b, m, l): records relative to 2^M and 2^m

@@ -149,6 +149,13 @@ __device__ __forceinline__ void st_chunk(uint8_t* tile, int row, int c, uint4 v)
 }
 
 // ---- planning: the groups and the stages that their rows need ----
+// A unit's length in the list: its stages, then kUnitCost places without one,
+// for what a unit costs beside its stages (Q, the end of its rows: 12 us, about
+// five stages).  Without them a CTA got 14 one-stage units of packed documents
+// while others got one unit of 14 stages: 379 us instead of 208.
+constexpr int kUnitCost = 4;
+__device__ __forceinline__ long long span_of(const WideUnit& u) { return u.n_stages + kUnitCost; }
+
 constexpr int kPlanThreads = 1024;
 
 // this phase's sequence i: rows (tokens) and keys
@@ -255,7 +262,7 @@ __global__ void __launch_bounds__(kPlanThreads) wide_plan_kernel(const __grid_co
     long long total = 0;
     for (int g0 = 0; g0 < n_groups; g0 += kPlanThreads) {
         const int g = g0 + tid;
-        const int n = g < n_groups ? a.units[g].n_stages : 0;
+        const long long n = g < n_groups ? span_of(a.units[g]) : 0;
         long long all;
         const long long upto = block_scan(n, sums, all);
         if (g < n_groups) a.units[g].before = total + upto - n;
@@ -267,22 +274,36 @@ __global__ void __launch_bounds__(kPlanThreads) wide_plan_kernel(const __grid_co
     }
 }
 
-// A CTA's (or a join's) way through the list.  Position x of the list of
-// n_kv * total stages lies in group g with n_kv * before_g <= x.
+// A CTA's (or a join's) way through the list.  Position x of the list, n_kv *
+// total long, lies in group g with n_kv * before_g <= x.
 struct Walk {
     WideUnit u;
     int group, h;             // group and kv head of the current unit
     long long unit0;          // list position of the unit's first stage
+    long long unit1, real1;   // of its end, and of the end of its stages
 };
 __device__ __forceinline__ bool walk_to(const AttendPagesArgs& a, Walk& w, long long x, int n_groups) {
     const int n_kv = a.pool.n_kv;
-    while (x >= n_kv * (w.u.before + w.u.n_stages)) {
+    while (x >= n_kv * (w.u.before + span_of(w.u))) {
         if (++w.group >= n_groups) return false;
         w.u = a.units[w.group];
     }
-    w.h = (int)((x - n_kv * w.u.before) / w.u.n_stages);
-    w.unit0 = n_kv * w.u.before + (long long)w.h * w.u.n_stages;
+    w.h = (int)((x - n_kv * w.u.before) / span_of(w.u));
+    w.unit0 = n_kv * w.u.before + w.h * span_of(w.u);
+    w.unit1 = w.unit0 + span_of(w.u);
+    w.real1 = w.unit0 + w.u.n_stages;
     return true;
+}
+// The next piece of the run [cur, run1): its first position and stages; cur moves
+// past it.  False at the end.
+__device__ __forceinline__ bool next_piece(const AttendPagesArgs& a, Walk& w, long long& cur, long long run1, int n_groups, long long& from, int& n_st) {
+    while (cur < run1 && walk_to(a, w, cur, n_groups)) {
+        from = cur;
+        cur = min(run1, w.unit1);
+        n_st = (int)(min(cur, w.real1) - from);
+        if (n_st > 0) return true;
+    }
+    return false;
 }
 // by a whole warp: the group of list position x
 __device__ __forceinline__ int find_group(const AttendPagesArgs& a, long long x, int n_groups) {
@@ -399,11 +420,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* sq = smem + kOffQ + tile * kTileBytes;
         const bool formed = a.softcap > 0.0f || a.slopes;
         uint32_t n_sub = 0;  // sub-stages of this tile so far: S, P and O phases go by it
-        for (long long cur = run0; cur < run1 && walk_to(a, w, cur, n_groups);) {
-            const long long unit1 = w.unit0 + w.u.n_stages, stop = min(run1, unit1);
-            const int n_st = (int)(stop - cur), st0 = w.u.stage0 + (int)(cur - w.unit0);
+        long long cur = run0, from = 0;
+        int n_st = 0;
+        while (next_piece(a, w, cur, run1, n_groups, from, n_st)) {
+            const int st0 = w.u.stage0 + (int)(from - w.unit0);
             const int tiles = w.u.rows > 128 ? 2 : 1;
-            cur = stop;
             if (tile >= tiles) continue;
             // ---- this thread's row ----
             const int r = tile * 128 + trow;
@@ -589,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             // ---- the piece's end: O through shared memory (this warp's rows of Q), 64
             // dims at a time, so that rows move as whole lines ----
-            const bool whole = w.unit0 >= run0 && unit1 <= run1;
+            const bool whole = w.unit0 >= run0 && w.real1 <= run1;
             const bool bad = bad_page || (!a.prefix_phase && end > (long long)a.batch.table_stride * kPageTokens);
             if (bad) l = CUDART_NAN_F;
             const int slot = w.unit0 < run0 ? 0 : 1;
@@ -621,50 +642,60 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto stage = [&](int row, int chunk) {
                 return reinterpret_cast<float4*>(sq + (row >> 4) * 16384 + (warp & 3) * 4096 + (row & 15) * 256 + ((chunk ^ (row & 15)) << 4));
             };
+            // where this thread's row goes, in values (-1: nowhere)
+            long long to = -1;
+            if (token >= 0)
+                to = final_rows ? token * a.out.row + head * a.out.head
+                                : (whole ? (long long)at * kHeadDim
+                                         : ((long long)(blockIdx.x * 2 + slot) * kWideRows + r) * kRecordFloats);
+            float* keep = whole ? a.prior_acc : a.records;
 #pragma unroll 1
             for (int hf = 0; hf < 2; ++hf) {
-                float o[64];
-                tmem_ld64(t_o + 64 * hf, o);
-                __syncwarp();
 #pragma unroll
-                for (int c = 0; c < 16; ++c)
-                    *stage(lane, c) = kNibbles ? make_float4(o[4 * c], o[4 * c + 2], o[4 * c + 1], o[4 * c + 3])
-                                               : make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                for (int c0 = 0; c0 < 64; c0 += 32) {
+                    float o[32];
+                    tmem_ld32(t_o + 64 * hf + c0, o);
+                    if (c0 == 0) __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        *stage(lane, c0 / 4 + c) = kNibbles ? make_float4(o[4 * c], o[4 * c + 2], o[4 * c + 1], o[4 * c + 3])
+                                                            : make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                }
                 __syncwarp();
-#pragma unroll 2
+                const int c = lane & 15, d = 64 * hf + 4 * c;
+                if (!final_rows) {
+#pragma unroll 4
+                    for (int it = 0; it < 16; ++it) {
+                        const int row = 2 * it + (lane >> 4);
+                        const long long rt = __shfl_sync(0xffffffffu, to, row);
+                        if (rt >= 0) *reinterpret_cast<float4*>(keep + rt + d) = *stage(row, c);
+                    }
+                    continue;
+                }
+#pragma unroll 4
                 for (int it = 0; it < 16; ++it) {
-                    const int row = 2 * it + (lane >> 4), c = lane & 15;
+                    const int row = 2 * it + (lane >> 4);
                     float4 v = *stage(row, c);
-                    const int tk = __shfl_sync(0xffffffffu, token, row), hd = __shfl_sync(0xffffffffu, head, row);
-                    const float fo = __shfl_sync(0xffffffffu, wo, row), fp = __shfl_sync(0xffffffffu, wp, row);
-                    const float LL = __shfl_sync(0xffffffffu, L, row);
-                    const bool fin = __shfl_sync(0xffffffffu, (int)finite, row) != 0;
-                    const size_t ra = (size_t)max(tk, 0) * a.n_qh + hd;
-                    const int d = 64 * hf + 4 * c;
-                    bool spoiled = false;
-                    if (tk >= 0) {
-                        if (final_rows) {
-                            float4 pv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            if (a.prefix_len > 0) pv = *reinterpret_cast<const float4*>(a.prior_acc + ra * kHeadDim + d);
-                            v.x = v.x * fo + pv.x * fp;
-                            v.y = v.y * fo + pv.y * fp;
-                            v.z = v.z * fo + pv.z * fp;
-                            v.w = v.w * fo + pv.w * fp;
-                            spoiled = fin && !((v.x + v.y + v.z + v.w) * 0.0f == 0.0f);
-                            if (LL == 0.0f) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            store_out4(a, tk, hd, d, v);
-                        } else if (whole) {
-                            *reinterpret_cast<float4*>(a.prior_acc + ra * kHeadDim + d) = v;
-                        } else {
-                            const int rr = tile * 128 + (warp & 3) * 32 + row;
-                            *reinterpret_cast<float4*>(a.records + ((size_t)(blockIdx.x * 2 + slot) * kWideRows + rr) * kRecordFloats + d) = v;
+                    const long long rt = __shfl_sync(0xffffffffu, to, row);
+                    const float fo = __shfl_sync(0xffffffffu, wo, row);
+                    // a part without weight (nothing of it is seen) does not count, whatever its sums hold
+                    v = fo == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(v.x * fo, v.y * fo, v.z * fo, v.w * fo);
+                    if (a.prefix_len > 0) {
+                        const float fp = __shfl_sync(0xffffffffu, wp, row);
+                        const unsigned long long ra = __shfl_sync(0xffffffffu, (unsigned long long)at, row);
+                        if (rt >= 0 && fp != 0.0f) {
+                            const float4 pv = *reinterpret_cast<const float4*>(a.prior_acc + ra * kHeadDim + d);
+                            v = make_float4(fmaf(pv.x, fp, v.x), fmaf(pv.y, fp, v.y), fmaf(pv.z, fp, v.z), fmaf(pv.w, fp, v.w));
                         }
                     }
-                    const uint32_t votes = __ballot_sync(0xffffffffu, spoiled && LL != 0.0f);
+                    const bool spoiled = rt >= 0 && !((v.x + v.y + v.z + v.w) * 0.0f == 0.0f);
+                    if (rt >= 0) store_out4_at(a, rt + d, v);
+                    const uint32_t votes = __ballot_sync(0xffffffffu, spoiled);
                     if (votes & 0xffffu) redo |= 1u << (2 * it);
                     if (votes >> 16) redo |= 2u << (2 * it);
                 }
             }
+            redo &= __ballot_sync(0xffffffffu, finite && L != 0.0f);
             for (; redo; redo &= redo - 1) {
                 const int row = __ffs(redo) - 1;
                 const int tk = __shfl_sync(0xffffffffu, token, row), hd = __shfl_sync(0xffffffffu, head, row);
@@ -689,17 +720,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             int hp, t0, valid;
             bool there;
         };
-        long long cur = run0, stop = run0;
-        int st = 0;
+        long long cur = run0;
+        int st = 0, left = 0;
         int pages = 0, pages_at = -1;
         const int* table = nullptr;
         int n_table = 0;
         auto advance = [&]() -> Next {
             Next x{nullptr, 0, 0, 0, false};
-            if (cur >= stop) {  // the next piece
-                if (cur >= run1 || !walk_to(a, w, cur, n_groups)) return x;
-                stop = min(run1, w.unit0 + w.u.n_stages);
-                st = w.u.stage0 + (int)(cur - w.unit0);
+            if (left == 0) {  // the next piece
+                long long from;
+                if (!next_piece(a, w, cur, run1, n_groups, from, left)) return x;
+                st = w.u.stage0 + (int)(from - w.unit0);
                 table = a.prefix_phase ? a.prefix_table : a.batch.table + (size_t)w.u.seq * a.batch.table_stride;
                 n_table = a.prefix_phase ? (a.prefix_len + kPageTokens - 1) / kPageTokens : a.batch.table_stride;
                 pages_at = -1;
@@ -717,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             x.valid = w.u.n_keys - st * kStageKeys;  // tokens of the stage that exist
             x.there = true;
             ++st;
-            ++cur;
+            --left;
             return x;
         };
         if (warp < kSoftWarps + kKWarps) {
@@ -887,11 +918,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t smem0 = smem_u32(smem);
         const uint64_t dq = desc_k(smem0 + kOffQ, 0), dk = desc_k(smem0 + kOffK, 0), dv = desc_mn(smem0 + kOffV, 0);
         uint32_t n_k = 0, n_v = 0, n_p[2] = {0, 0}, n_q[2] = {0, 0};
-        for (long long cur = run0; ok && cur < run1 && walk_to(a, w, cur, n_groups);) {
-            const long long stop = min(run1, w.unit0 + w.u.n_stages);
-            const int n_st = (int)(stop - cur);
+        long long cur = run0, from = 0;
+        int n_st = 0;
+        while (ok && next_piece(a, w, cur, run1, n_groups, from, n_st)) {
             const int tiles = w.u.rows > 128 ? 2 : 1;
-            cur = stop;
             // S of a sub-stage of tile t: 64 keys, half of the stage's K tile
             auto scores = [&](int t, uint32_t half) {
                 const uint64_t k = dk + ((n_k & 1) * kTileBytes + half * (kSubKeys * 128)) / 16;
@@ -972,9 +1002,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) wide_join_kernel(const __grid
     Walk w;
     w.group = find_group(a, x, n_groups);
     w.u = a.units[w.group];
-    if (!walk_to(a, w, x, n_groups) || w.unit0 == x || w.unit0 < x - per) return;  // between units, or not the first border
-    const long long unit1 = w.unit0 + w.u.n_stages;
-    const int c0 = blockIdx.x, c1 = (int)((unit1 - 1) / per);
+    // between units or behind a unit's stages, or not the unit's first border
+    if (!walk_to(a, w, x, n_groups) || w.unit0 == x || x >= w.real1 || w.unit0 < x - per) return;
+    const int c0 = blockIdx.x, c1 = (int)((w.real1 - 1) / per);
     const int ft = a.prefix_phase ? 0 : a.batch.q_start[w.u.seq];
     for (int r = blockIdx.y * kJoinWarps + warp; r < w.u.rows; r += gridDim.y * kJoinWarps) {
         const int fr = w.u.row0 + r, token = ft + fr / a.group, head = w.h * a.group + fr % a.group;
