@@ -234,20 +234,28 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_pages_kernel(const A
     auto rotate = [&](float (&x)[4]) {
         if (a.rot == 0) return;  // uniform
         float y[4];
+        if (a.interleaved) {  // the lane's own other element
+            y[0] = x[1]; y[1] = x[0]; y[2] = x[3]; y[3] = x[2];
+        } else if ((half & 3) == 0) {  // the same element of one other lane
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            // the partner's value: lane partner/4, element partner%4 (the same for no
-            // two elements in general, so all four are fetched and one picked)
-            const int from = partner[u] >> 2, el = partner[u] & 3;
-            float v[4];
+            for (int u = 0; u < 4; ++u) y[u] = __shfl_sync(0xffffffffu, x[u], partner[0] >> 2);
+        } else {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) v[w] = __shfl_sync(0xffffffffu, x[w], from);
-            y[u] = el == 0 ? v[0] : (el == 1 ? v[1] : (el == 2 ? v[2] : v[3]));
+            for (int u = 0; u < 4; ++u) {
+                // lane partner/4, element partner%4: the same for no two elements in
+                // general, so all four are fetched and one picked
+                const int from = partner[u] >> 2, el = partner[u] & 3;
+                float v[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) v[w] = __shfl_sync(0xffffffffu, x[w], from);
+                y[u] = el == 0 ? v[0] : (el == 1 ? v[1] : (el == 2 ? v[2] : v[3]));
+            }
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u)
             if (4 * lane + u < a.rot) x[u] = (float)(c[u] * (double)x[u] + s[u] * (double)y[u]);
     };
+#pragma unroll 2
     for (int h = h0 + warp; h < h1; h += kAppendWarps) {
         float x[4];
         if (h < n_kv) {
