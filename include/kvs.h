@@ -456,7 +456,7 @@ typedef struct kvs_page_pool {
  * Q and output tensors as its new tokens, which sit at the end of its
  * seq_len[i] cached tokens (new token t of n at own position seq_len[i] - n +
  * t), and its tokens 256 j .. 256 j + 255 in page page_table[i][j].  Rows
- * outside every sequence's range (padding) are neither read nor written.
+ * outside every sequence's range (padding) get nothing written.
  * q_start does not decrease.  Sequences may have no rows and no tokens.  More
  * rows than tokens is allowed: rows at negative positions append nothing, and
  * see nothing of their own pages. */
@@ -470,7 +470,10 @@ typedef struct kvs_page_batch {
     const int* page_table; /* device [n_seqs][table_stride] */
     int table_stride;      /* page table entries per sequence; those past a sequence's
                               last page may hold anything */
-    int* status;           /* device word that KVS_ERR_* bits are or-ed into, or NULL */
+    int* status;           /* device word that KVS_ERR_* bits are or-ed into, or NULL (a bad page, or
+                              a bounded wait inside a kernel that gave up: the GPU stalled for
+                              10 s, the outputs are incomplete and the workspace has to be
+                              zeroed again) */
 } kvs_page_batch;
 
 /* A [n_rows][heads][128] tensor of KVS_DT_* values with its strides, in
@@ -548,7 +551,11 @@ int kvs_read_pages(const kvs_page_pool* pool, const kvs_page_batch* batch, int d
  * as two 16-bit terms unless out is BF16, so that an F32 or F16 result has
  * fp32-class accuracy with every V type but Q4_1 and Q5_1 (whose values are
  * rounded to fp16); wider rows use the tcgen05 tensor cores with K, V and
- * probabilities rounded to fp16 once each.
+ * probabilities rounded to fp16 once each (a K value beyond fp16's range, which
+ * only bf16 or fp32 input can bring, makes the rows that see it NaN there).
+ * out must not overlap q.  q_start, lengths and tables may change between
+ * replays of a captured call, the batch's bounds (n_seqs, n_rows, max_new) and
+ * addresses may not.
  *
  * workspace: device, 256-byte aligned, at least kvs_attend_pages_workspace
  * bytes, zero-filled once before its first use; every call leaves it ready for

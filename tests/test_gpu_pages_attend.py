@@ -270,3 +270,89 @@ def test_append_then_attend_as_a_serving_loop():
         t.cuda.synchronize()
         b.pool = b.d_pool.cpu().numpy()
         check(b, q.double().cpu().numpy(), out, lse, wide=max(new) * 2 > 32)
+
+
+def test_many_short_sequences_and_an_empty_batch():
+    """More sequences than a warp scans at once, most without rows or tokens."""
+    t = torch()
+    rng = np.random.default_rng(24)
+    new = [int(x) for x in rng.choice([0, 0, 1, 2], 300)]
+    lens = [max(n, int(x)) for n, x in zip(new, rng.choice([0, 1, 40, 130], 300))]
+    b = Batch(new, lens, 2, 1, (Q8_0, Q4_0), pad=2, seed=24).device()
+    check(b, *run(b, "float16", "float32"))
+    none = b.kvs.make_page_batch(b.d["start"][:1], b.d["lens"][:0], b.d["table"][:0], 4)
+    out = t.full((4, 2, 128), 5.0, device="cuda")
+    q = t.zeros(4, 2, 128, dtype=t.float16, device="cuda")
+    b.kvs.kvs_attend_pages(b.c_pool, none, q, out, None, None, None, b.workspace())
+    b.kvs.kvs_read_pages(b.c_pool, none, out[:, :1])
+    t.cuda.synchronize()
+    assert bool((out == 5).all())
+
+
+def test_two_streams_with_a_workspace_each():
+    """Two calls in flight at once do not disturb each other."""
+    t = torch()
+    pair = [Batch([1] * 4, [2000, 300, 5, 900], 8, 2, (Q8_0, Q4_0), prefix=p, seed=25 + p).device() for p in (0, 500)]
+    alone = [run(b, "bfloat16") for b in pair]
+    streams = [t.cuda.Stream() for _ in pair]
+    works = [b.workspace() for b in pair]
+    qs = [t.from_numpy(b.q).bfloat16().cuda() for b in pair]
+    outs = [t.zeros(b.rows, 8, 128, dtype=t.bfloat16, device="cuda") for b in pair]
+    t.cuda.synchronize()
+    for _ in range(10):
+        for b, s, w, q, o in zip(pair, streams, works, qs, outs):
+            b.kvs.kvs_attend_pages(b.c_pool, b.c_batch, q, o, None, None, b.c_prefix, w, s)
+    t.cuda.synchronize()
+    for a, o in zip(alone, outs):
+        assert t.equal(a[1], o)
+
+
+def test_first_call_of_a_process_may_be_captured():
+    """No lazy set-up of the calls needs a run outside a capture."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import sys
+sys.path[:0] = ['tests', '.']
+import torch as t
+from pages_testlib import Batch
+b = Batch([1, 40], [300, 200], 4, 2, (8, 2), prefix=100, seed=26).device()
+q = t.from_numpy(b.q).half().cuda(); out = t.zeros(b.rows, 4, 128, device='cuda'); kv = t.zeros(b.rows, 2, 128, device='cuda')
+w = b.workspace(); s = t.cuda.Stream(); t.cuda.synchronize()
+g = t.cuda.CUDAGraph()
+with t.cuda.graph(g, stream=s):
+    b.kvs.kvs_read_pages(b.c_pool, b.c_batch, kv, stream=s)
+    b.kvs.kvs_append_pages(b.c_pool, b.c_batch, kv, kv, stream=s)
+    b.kvs.kvs_attend_pages(b.c_pool, b.c_batch, q, out, None, None, b.c_prefix, w, s)
+g.replay(); t.cuda.synchronize()
+first = out.clone(); out.zero_()
+b.kvs.kvs_attend_pages(b.c_pool, b.c_batch, q, out, None, None, b.c_prefix, w); t.cuda.synchronize()
+assert t.equal(first, out) and float(out.abs().sum()) > 0
+print('captured')
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_binding_refuses_wrong_tensors():
+    t = torch()
+    b = Batch([2, 1], [100, 300], 4, 2, (Q8_0, Q4_0), seed=27).device()
+    q = t.zeros(b.rows, 4, 128, dtype=t.float16, device="cuda")
+    w = b.workspace()
+    bad = [dict(q=q[:2]), dict(q=q[:, :3]), dict(q=q.float()), dict(q=q[:, :, :64]), dict(q=q.cpu()), dict(out=q.to(t.int32)),
+           dict(q=t.zeros(b.rows, 128, 4, dtype=t.float16, device="cuda").transpose(1, 2)), dict(lse=t.zeros(2, 4, device="cuda")),
+           dict(workspace=None), dict(workspace=w[:1000]), dict(score=b.kvs.make_score(alibi_slopes=t.ones(3, device="cuda"))),
+           dict(score=b.kvs.make_score(first_key=t.zeros(2, dtype=t.int32, device="cuda")))]
+    for kw in bad:
+        args = dict(q=q, out=t.zeros_like(q), lse=None, score=None, prefix=None, workspace=w)
+        args.update(kw)
+        with pytest.raises(b.kvs.KvsError):
+            b.kvs.kvs_attend_pages(b.c_pool, b.c_batch, **args)
+    for make in (lambda: b.kvs.make_page_pool(b.d_pool.flatten()[:-1], 2), lambda: b.kvs.make_page_prefix(b.d["lens"][:1], 300),
+                 lambda: b.kvs.make_page_batch(b.d["start"][:2], b.d["lens"], b.d["table"], 3),
+                 lambda: b.kvs.make_page_batch(b.d["start"].long(), b.d["lens"], b.d["table"], 3),
+                 lambda: b.kvs.make_rope(t.ones(10, device="cuda"), 64)):
+        with pytest.raises(b.kvs.KvsError):
+            make()
