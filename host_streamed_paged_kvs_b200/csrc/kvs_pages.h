@@ -106,7 +106,7 @@ inline long long wide_groups(long long n_rows, int group, long long n_seqs) {
 constexpr int kFewRowsMax = 16;
 constexpr int kFewSeqRows = 32;
 constexpr int kRecordFloats = 132;      // 128 sums, reference, sum of weights, padding
-constexpr int kFewCtas = 444;           // up to three per SM
+constexpr int kFewCtas = 296;           // two per SM
 constexpr size_t kFewRecordBytes = (size_t)kFewCtas * 2 * kFewRowsMax * kRecordFloats * 4;
 
 struct PageMaps {
