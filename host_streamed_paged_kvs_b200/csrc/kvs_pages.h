@@ -172,7 +172,8 @@ __device__ __forceinline__ RowView row_view(const AttendPagesArgs& a, int seq, i
     v.first = a.first_key ? a.first_key[row] : (a.window > 0 ? v.pos - a.window + 1 : 0);
     v.end = a.end_key ? a.end_key[row] : v.pos + 1;
     v.first = max(v.first, 0);
-    v.end = min(v.end, a.prefix_len + len);
+    // 0 .. the keys that exist: callers subtract the prefix from it, which an end far below 0 would not survive
+    v.end = max(0, (int)min((long long)v.end, (long long)a.prefix_len + len));
     return v;
 }
 

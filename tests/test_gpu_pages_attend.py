@@ -356,3 +356,18 @@ def test_binding_refuses_wrong_tensors():
                  lambda: b.kvs.make_rope(t.ones(10, device="cuda"), 64)):
         with pytest.raises(b.kvs.KvsError):
             make()
+
+
+@pytest.mark.parametrize("new", [3, 40], ids=["few-rows", "many-rows"])
+def test_extreme_intervals_beside_a_prefix(new):
+    """Ends at the lowest int32 and starts at the highest see nothing, also where
+    the prefix is subtracted from them."""
+    t = torch()
+    b = Batch([new], [200], 2, 1, (Q8_0, Q4_0), prefix=150, seed=28).device()
+    first, end = np.zeros(new, np.int32), np.full(new, 2 ** 31 - 1, np.int32)
+    end[0], first[1] = -2 ** 31, 2 ** 31 - 1
+    first[2], end[2] = -2 ** 31, 151
+    score = b.kvs.make_score(first_key=t.from_numpy(first).cuda(), end_key=t.from_numpy(end).cuda())
+    q64, out, lse = run(b, "float16", "float32", score=score)
+    check(b, q64, out, lse, wide=new > 16, first=first, end=end)
+    assert bool((out[:2] == 0).all()) and bool((lse[:2] == -math.inf).all())
