@@ -87,7 +87,7 @@ struct AttendPagesArgs {
 struct WideUnit {
     int seq, row0, rows;     // rows row0 .. row0 + rows - 1 of the sequence, token-major
     int stage0, n_stages;    // at least 1
-    int n_keys;              // keys that exist
+    int n_keys;              // keys that exist; 0 where no row sees any
     long long before;        // length of the groups before this one in the list
 };
 struct WidePlan {

@@ -247,6 +247,9 @@ __global__ void __launch_bounds__(kPlanThreads) wide_plan_kernel(const __grid_co
                 from = min(from, __shfl_xor_sync(0xffffffffu, from, off));
                 to = max(to, __shfl_xor_sync(0xffffffffu, to, off));
             }
+            // A group that sees no key has one stage of no keys: none of its page numbers is
+            // judged (released pages may stand there), and its values count as 0
+            if (from >= to) u.n_keys = 0;
             // keys beyond the page table are nobody's: such a unit comes out as NaN
             if (!a.prefix_phase) to = (int)min((long long)to, (long long)a.batch.table_stride * kPageTokens);
             u.stage0 = from < to ? from / kStageKeys : 0;
