@@ -702,7 +702,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int sq_ = __shfl_sync(0xffffffffu, seq, row);
                 store_out4(a, tk, hd, 4 * lane, slow_row<VT, KT>(a, sq_, tk, hd));
             }
-            if (bad && lane == 0 && a.batch.status) atomicOr(a.batch.status, kErrBadPage);
+            // any row of the warp: a row that ends beyond the table may be in any lane
+            if (__any_sync(0xffffffffu, bad) && lane == 0 && a.batch.status) atomicOr(a.batch.status, kErrBadPage);
             __syncwarp();
         }
     } else if (warp < kMmaWarp) {

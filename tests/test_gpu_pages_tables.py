@@ -58,3 +58,15 @@ def test_intervals_that_end_inside_the_prefix(new):
     q64, out, lse = run(b, "float16", "float32", score=b.kvs.make_score(first_key=ints(end), end_key=ints(end)))
     assert int(b.status) == 0
     check(b, q64, out, lse, wide=new > 16, first=end, end=end)
+
+
+@pytest.mark.parametrize("new,group,over", [(40, 1, 3), (40, 1, 1), (70, 1, 33), (17, 2, 1)])
+def test_status_of_rows_beyond_the_page_table(new, group, over):
+    """The last rows end behind the table's last entry: NaN and the status bit,
+    whichever lanes and warps hold them."""
+    b = Batch([new], [512], group, 1, (Q8_0, Q4_0), pad=1, seed=56, extra_cols=0).device(status=True)
+    b.d["lens"].fill_(512 + over)
+    q64, out, lse = run(b, "float16", "float32")
+    assert int(b.status) == b.kvs.KVS_ERR_BAD_PAGE
+    end = np.minimum(512 + over - new + 1 + np.arange(b.rows), 600)
+    check_where(b, range(new - over, new), q64, out, lse, new * group > 32, end=end)
