@@ -73,7 +73,7 @@ struct Piece {
     int n_keys;               // keys that exist
     int slot;                 // record slot, or -1: the whole unit is here
     int cta0, n_ctas;         // CTAs that share the unit
-    volatile int bad;         // a page number was outside the pool
+    volatile int bad;         // a page number of its stages was outside the pool, or some row ends beyond the table
     int pages[32];            // the first pages, from first_stage / 2 on
     int token[ROWS], head[ROWS];
     int pos[ROWS], first[ROWS], end[ROWS];  // in keys of this phase
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                 if (!ok) break;
                 if (lane == 0) {
                     if ((unsigned)page >= (unsigned)a.pool.n_pages) {
-                        page = 0;  // some page: its piece comes out as NaN
+                        page = 0;  // some page: rows that see it come out as NaN
                         p.bad = 1;
                     }
                     uint8_t* dst = smem + buf * G::kBytes;
@@ -844,8 +844,17 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
         }
 
         // ---- the piece's end ----
+        // Where a page number is bad each row judges the keys that it sees
         const bool bad = p.bad;
-        if (bad && tid == 0 && a.batch.status) atomicOr(a.batch.status, kErrBadPage);
+        auto row_bad = [&](int r) -> bool {
+            if (!bad) return false;
+            const int* table = a.prefix_phase ? a.prefix_table : a.batch.table + (size_t)p.seq * a.batch.table_stride;
+            const int n_table = a.prefix_phase ? (a.prefix_len + kPageTokens - 1) / kPageTokens : a.batch.table_stride;
+            const bool sees = sees_bad_page(table, n_table, a.pool.n_pages, p.first[r], p.end[r], p.first_stage * kStageKeys,
+                                            (p.first_stage + p.n_stages) * kStageKeys);
+            if (sees && a.batch.status) atomicOr(a.batch.status, kErrBadPage);
+            return sees;
+        };
         // What the prefix left for this warp's two rows of 8 nt .. + 7, on its way early
         float4 pacc[2];
         float2 pml[2];
@@ -897,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                 sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                 if (g == 0) {
                     sml[(warp * 8 + 2 * q + jr) * 2] = ref[nt][jr];
-                    sml[(warp * 8 + 2 * q + jr) * 2 + 1] = bad ? CUDART_NAN_F : sum;
+                    sml[(warp * 8 + 2 * q + jr) * 2 + 1] = row_bad(8 * nt + 2 * q + jr) ? CUDART_NAN_F : sum;
                 }
                 float* dst = red + (warp * 8 + 2 * q + jr) * kRedRow;
 #pragma unroll

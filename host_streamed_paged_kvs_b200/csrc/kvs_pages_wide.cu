@@ -485,14 +485,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) arrive(&q_full[tile]);
-            // page numbers outside the pool: the piece comes out as NaN
-            bool bad_page = false;
+            // A row that sees a key of a page outside the pool, or beyond the page table,
+            // comes out as NaN.  Rarely are there such pages among the piece's: then
+            // each row judges those it sees.
+            bool bad = false;
             {
                 const int* table = a.prefix_phase ? a.prefix_table : a.batch.table + (size_t)w.u.seq * a.batch.table_stride;
                 const int n_table = a.prefix_phase ? (a.prefix_len + kPageTokens - 1) / kPageTokens : a.batch.table_stride;
+                bool some = !a.prefix_phase && max((long long)first, (long long)n_table * kPageTokens) < end;
                 for (int j = (st0 >> 1) + lane; 2 * j < st0 + n_st && j * kPageTokens < w.u.n_keys; j += 32)
-                    bad_page |= j >= n_table || (unsigned)table[j] >= (unsigned)a.pool.n_pages;
-                bad_page = __any_sync(0xffffffffu, bad_page);
+                    some |= j >= n_table || (unsigned)table[j] >= (unsigned)a.pool.n_pages;
+                if (__any_sync(0xffffffffu, some))
+                    bad = sees_bad_page(table, n_table, a.pool.n_pages, first, end, st0 * kStageKeys, (st0 + n_st) * kStageKeys);
             }
 
             float ref = token >= 0 ? -CUDART_INF_F : 0.0f, l = 0.0f;
@@ -611,7 +615,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- the piece's end: O through shared memory (this warp's rows of Q), 64
             // dims at a time, so that rows move as whole lines ----
             const bool whole = w.unit0 >= run0 && w.real1 <= run1;
-            const bool bad = bad_page || (!a.prefix_phase && end > (long long)a.batch.table_stride * kPageTokens);
             if (bad) l = CUDART_NAN_F;
             const int slot = w.unit0 < run0 ? 0 : 1;
             const size_t at = (size_t)max(token, 0) * a.n_qh + head;

@@ -429,9 +429,11 @@ int kvs_attend_pages_static(const void* pages, int n_pages, int n_tokens, int n_
  * misaligned pointers, negative sizes, unsupported types, strides that the
  * vector accesses cannot take.  What only the device can see is bounded
  * there: rows beyond n_rows, lengths beyond the page table and page numbers
- * outside the pool are never followed.  A bad page number gives NaN in the
- * rows of a sequence (of the batch, for the prefix) that would have read the
- * page, is not written by an append, and sets KVS_ERR_BAD_PAGE in *status.
+ * outside the pool are never followed.  A row that sees a key (or is itself a
+ * token) of a page with a bad number, or beyond its page table, becomes NaN
+ * where it would be read, is not written by an append, and sets
+ * KVS_ERR_BAD_PAGE in *status.  Table entries of pages that no row sees (those
+ * before a window, say) may hold anything.
  *
  * All device pointers of a call belong to one device, the one that owns
  * pool->pages; it need not be the current one.  `stream` must be a stream of

@@ -70,3 +70,72 @@ def test_status_of_rows_beyond_the_page_table(new, group, over):
     assert int(b.status) == b.kvs.KVS_ERR_BAD_PAGE
     end = np.minimum(512 + over - new + 1 + np.arange(b.rows), 600)
     check_where(b, range(new - over, new), q64, out, lse, new * group > 32, end=end)
+
+
+@pytest.mark.parametrize("new", [6, 40], ids=["few-rows", "many-rows"])
+@pytest.mark.parametrize("types", [(Q8_0, Q4_0), (F16, F16)], ids=["q8-q4_0", "f16-f16"])
+def test_only_rows_that_see_a_bad_page_are_nan(new, types):
+    """Bad own pages and a bad prefix page, seen by some rows of a tile only."""
+    b = Batch([new, new], [600, 530], 2, 1, types, prefix=600, pad=1, seed=53).device(status=True)
+    b.d["ptable"][1] = b.n_pages               # keys 256..511
+    b.d["table"][0, 0] = -1                    # keys 600..855 of sequence 0
+    b.d["table"][1, 1] = 2 ** 31 - 1           # keys 856..1111 of sequence 1
+    first, end = np.full(b.rows, 856, np.int32), np.full(b.rows, 10 ** 6, np.int32)
+    first[0] = 511                             # the bad prefix page's last key
+    first[1], end[1] = 512, 600                # the prefix behind it
+    first[2], end[2] = 0, 256                  # and before it
+    first[3] = 855                             # the bad own page's last key
+    first[4], end[4] = 700, 700                # nothing, inside the bad page
+    first[new:], end[new:] = 600, 856          # sequence 1 before its bad page
+    first[new], end[new] = 300, 601
+    end[new + 1] = 857
+    first[new + 2] = 1112
+    bad = [0, 3, new, new + 1]
+    q64, out, lse = run(b, "float16", "float32", score=b.kvs.make_score(first_key=ints(first), end_key=ints(end)))
+    assert int(b.status) == b.kvs.KVS_ERR_BAD_PAGE
+    check_where(b, bad, q64, out, lse, new > 16, first=first, end=end)
+
+
+@pytest.mark.parametrize("new", [2, 40], ids=["few-rows", "many-rows"])
+def test_a_bad_page_between_the_rows_intervals(new):
+    """Two rows of one tile with a page between their intervals that neither sees."""
+    b = Batch([new], [900], 2, 1, (Q8_0, Q4_0), seed=54).device(status=True)
+    b.d["table"][0, 1:3] = -1
+    first, end = np.zeros(new, np.int32), np.full(new, 256, np.int32)
+    first[new // 2:], end[new // 2:] = 768, 900
+    q64, out, lse = run(b, "float16", "float32", score=b.kvs.make_score(first_key=ints(first), end_key=ints(end)))
+    assert int(b.status) == 0
+    check(b, q64, out, lse, wide=new > 16, first=first, end=end)
+
+
+@pytest.mark.parametrize("new", [3, 40], ids=["few-rows", "many-rows"])
+def test_a_window_that_leaves_the_bad_page_out(new):
+    b = Batch([new, new], [700, 650], 2, 1, (Q8_0, Q4_0), seed=55).device(status=True)
+    b.d["table"][:, 0] = b.n_pages + 3
+    q64, out, lse = run(b, "float16", "float32", score=b.kvs.make_score(window=340))
+    assert int(b.status) == 0
+    check(b, q64, out, lse, wide=new > 16, window=340)
+    # the first rows of the second sequence see the page's last key again
+    window = 650 - new + 1 - 255
+    q64, out, lse = run(b, "float16", "float32", score=b.kvs.make_score(window=window))
+    assert int(b.status) == b.kvs.KVS_ERR_BAD_PAGE
+    check_where(b, [new], q64, out, lse, new > 16, window=window)
+
+
+def test_length_hint_below_the_truth():
+    """max_new says one row a sequence, two have more: right, by the few-row kernel."""
+    for n in (20, 70):
+        b = Batch([n, 1, 12], [500, 300, 20], 4, 2, (Q8_0, Q4_0), prefix=60, pad=3, seed=57).device(max_new=1)
+        check(b, *run(b, "float16", "float32"), wide=True)
+        b = Batch([n, 1, 12], [500, 300, 20], 4, 2, (Q8_0, Q4_0), pad=3, seed=58).device(max_new=1)
+        check(b, *run(b, "float16", "float32"))
+
+
+def test_status_of_few_rows_beyond_the_page_table():
+    """The same by the few-row kernel: the rows inside the table keep their values."""
+    b = Batch([6, 1], [512, 300], 2, 1, (Q8_0, Q4_0), pad=1, seed=59, extra_cols=0).device(status=True)
+    b.d["lens"][0] = 514
+    q64, out, lse = run(b, "float16", "float32")
+    assert int(b.status) == b.kvs.KVS_ERR_BAD_PAGE
+    end = np.array([509 + i for i in range(6)] + [300, 0])
+    check_where(b, [4, 5], q64, out, lse, False, end=end)
