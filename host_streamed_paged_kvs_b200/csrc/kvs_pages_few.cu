@@ -73,7 +73,7 @@ struct Piece {
     int n_keys;               // keys that exist
     int slot;                 // record slot, or -1: the whole unit is here
     int cta0, n_ctas;         // CTAs that share the unit
-    volatile int bad;         // a page number of its stages was outside the pool, or some row ends beyond the table
+    uint32_t nan_rows;        // rows that see a page outside the pool, or a key beyond the table, a bit each
     int pages[32];            // the first pages, from first_stage / 2 on
     int token[ROWS], head[ROWS];
     int pos[ROWS], first[ROWS], end[ROWS];  // in keys of this phase
@@ -349,16 +349,25 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                 p.full_from = full_from;
                 p.full_to = full_to;
                 p.n_keys = s.n_keys;
-                // a row that may see keys beyond the page table
-                p.bad = hi > (long long)a.batch.table_stride * kPageTokens && !a.prefix_phase;
             }
             // the first pages' numbers
             const int* table = a.prefix_phase ? a.prefix_table : a.batch.table + (size_t)seq * a.batch.table_stride;
             const int n_table = a.prefix_phase ? (a.prefix_len + kPageTokens - 1) / kPageTokens : a.batch.table_stride;
             const int j = (st0 >> 1) + lane;
-            p.pages[lane] = 2 * j < st1 && j < n_table ? table[j] : -1;
+            const int page = 2 * j < st1 && j < n_table ? table[j] : -1;
+            p.pages[lane] = page;
             __syncwarp();
             if (lane == 0) arrive(&p_meta[slot]);
+            // Where the piece's pages hold a bad number, or a row ends beyond the table, each
+            // row judges the keys that it sees
+            bool some = max((long long)first, (long long)n_table * kPageTokens) < end || (2 * j < st1 && (unsigned)page >= (unsigned)a.pool.n_pages);
+            for (int i = j + 32; 2 * i < st1; i += 32) some |= i >= n_table || (unsigned)table[i] >= (unsigned)a.pool.n_pages;
+            uint32_t nan_rows = 0;
+            if (__any_sync(0xffffffffu, some)) {
+                nan_rows = __ballot_sync(0xffffffffu, sees_bad_page(table, n_table, a.pool.n_pages, first, end, st0 * kStageKeys, st1 * kStageKeys));
+                if (nan_rows && lane == 0 && a.batch.status) atomicOr(a.batch.status, kErrBadPage);
+            }
+            if (lane == 0) p.nan_rows = nan_rows;
             if (lane == 0) {
                 // the record slot, and the CTAs that share the unit
                 p.slot = (unit0 >= run0 && unit1 <= run1) ? -1 : (unit0 < run0 ? 0 : 1);
@@ -442,10 +451,7 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                 ok = __all_sync(0xffffffffu, wait_phase(&empty[buf], buf_phase, a.batch.status));
                 if (!ok) break;
                 if (lane == 0) {
-                    if ((unsigned)page >= (unsigned)a.pool.n_pages) {
-                        page = 0;  // some page: rows that see it come out as NaN
-                        p.bad = 1;
-                    }
+                    if ((unsigned)page >= (unsigned)a.pool.n_pages) page = 0;  // some page: rows that see it come out as NaN
                     uint8_t* dst = smem + buf * G::kBytes;
                     uint64_t* bar = &full[buf];
                     mbar_expect_tx(bar, G::kBytes);
@@ -844,17 +850,6 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
         }
 
         // ---- the piece's end ----
-        // Where a page number is bad each row judges the keys that it sees
-        const bool bad = p.bad;
-        auto row_bad = [&](int r) -> bool {
-            if (!bad) return false;
-            const int* table = a.prefix_phase ? a.prefix_table : a.batch.table + (size_t)p.seq * a.batch.table_stride;
-            const int n_table = a.prefix_phase ? (a.prefix_len + kPageTokens - 1) / kPageTokens : a.batch.table_stride;
-            const bool sees = sees_bad_page(table, n_table, a.pool.n_pages, p.first[r], p.end[r], p.first_stage * kStageKeys,
-                                            (p.first_stage + p.n_stages) * kStageKeys);
-            if (sees && a.batch.status) atomicOr(a.batch.status, kErrBadPage);
-            return sees;
-        };
         // What the prefix left for this warp's two rows of 8 nt .. + 7, on its way early
         float4 pacc[2];
         float2 pml[2];
@@ -906,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                 sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                 if (g == 0) {
                     sml[(warp * 8 + 2 * q + jr) * 2] = ref[nt][jr];
-                    sml[(warp * 8 + 2 * q + jr) * 2 + 1] = row_bad(8 * nt + 2 * q + jr) ? CUDART_NAN_F : sum;
+                    sml[(warp * 8 + 2 * q + jr) * 2 + 1] = (p.nan_rows >> (8 * nt + 2 * q + jr)) & 1u ? CUDART_NAN_F : sum;
                 }
                 float* dst = red + (warp * 8 + 2 * q + jr) * kRedRow;
 #pragma unroll

@@ -33,7 +33,7 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int* 
 // Whether a row that sees the keys first .. end - 1 (of this phase's table) sees
 // one beyond the table, or one of the keys from .. to - 1 whose page is not in the
 // pool.  Called where some page number is known to be bad, so plain loads will do.
-static __device__ __noinline__ bool sees_bad_page(const int* table, int n_table, int n_pages, int first, int end, int from, int to) {
+__device__ __forceinline__ bool sees_bad_page(const int* table, int n_table, int n_pages, int first, int end, int from, int to) {
     if (max((long long)first, (long long)n_table * kPageTokens) < end) return true;
     const int k0 = max(first, from), k1 = min(end, to);
     if (k0 < k1)
