@@ -466,7 +466,8 @@ typedef struct kvs_page_batch {
     int n_seqs;            /* >= 0 */
     int n_rows;            /* rows of the tensors; a bound on q_start[n_seqs] */
     int max_new;           /* rows of the longest sequence, if known (0 = not known): kernels are
-                              chosen by it; a sequence with more rows is right, only slower */
+                              chosen by it; a sequence with more rows is right, only slower.  A
+                              batch of one sequence is taken to have max_new rows, if given */
     const int* q_start;    /* device [n_seqs + 1] */
     const int* seq_len;    /* device [n_seqs], tokens after the append */
     const int* page_table; /* device [n_seqs][table_stride] */
