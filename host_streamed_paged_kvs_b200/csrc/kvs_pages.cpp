@@ -111,9 +111,10 @@ int check_batch(const kvs_page_batch* b, PageBatch* out) {
 
 bool dtype_ok(int d) { return d == KVS_DT_F16 || d == KVS_DT_BF16 || d == KVS_DT_F32; }
 
-int check_rows(const kvs_page_rows* r, int dtype, const char* what, RowsRef* out) {
+// n_rows: of the batch; a tensor of no rows may have a null address
+int check_rows(const kvs_page_rows* r, int dtype, int n_rows, const char* what, RowsRef* out) {
     static thread_local char msg[128];
-    if (!r || !r->data) {
+    if (!r || (!r->data && n_rows > 0)) {
         snprintf(msg, sizeof msg, "null %s", what);
         return fail(KVS_E_INVAL, msg);
     }
@@ -155,11 +156,11 @@ extern "C" int kvs_append_pages(const kvs_page_pool* pool, const kvs_page_batch*
     if (rc == KVS_OK) rc = check_batch(batch, &a.batch);
     if (rc != KVS_OK) return rc;
     if (!dtype_ok(dtype)) return fail(KVS_E_INVAL, "unknown dtype");
-    if ((rc = check_rows(k, dtype, "k", &a.k)) != KVS_OK || (rc = check_rows(v, dtype, "v", &a.v)) != KVS_OK) return rc;
+    if ((rc = check_rows(k, dtype, batch->n_rows, "k", &a.k)) != KVS_OK || (rc = check_rows(v, dtype, batch->n_rows, "v", &a.v)) != KVS_OK) return rc;
     if ((q == nullptr) != (q_out == nullptr)) return fail(KVS_E_INVAL, "q and q_out go together");
     if (q) {
         if (n_q_heads < 1) return fail(KVS_E_INVAL, "n_q_heads must be positive when q is given");
-        if ((rc = check_rows(q, dtype, "q", &a.q)) != KVS_OK || (rc = check_rows(q_out, dtype, "q_out", &a.q_out)) != KVS_OK) return rc;
+        if ((rc = check_rows(q, dtype, batch->n_rows, "q", &a.q)) != KVS_OK || (rc = check_rows(q_out, dtype, batch->n_rows, "q_out", &a.q_out)) != KVS_OK) return rc;
         a.n_qh = n_q_heads;
     }
     if ((long long)a.pool.n_kv + a.n_qh > 65535) return fail(KVS_E_INVAL, "more than 65535 heads");
@@ -189,8 +190,8 @@ extern "C" int kvs_read_pages(const kvs_page_pool* pool, const kvs_page_batch* b
     if (rc != KVS_OK) return rc;
     if (!dtype_ok(dtype)) return fail(KVS_E_INVAL, "unknown dtype");
     if (!k && !v) return fail(KVS_E_INVAL, "neither k nor v is wanted");
-    if (k && (rc = check_rows(k, dtype, "k", &a.k)) != KVS_OK) return rc;
-    if (v && (rc = check_rows(v, dtype, "v", &a.v)) != KVS_OK) return rc;
+    if (k && (rc = check_rows(k, dtype, batch->n_rows, "k", &a.k)) != KVS_OK) return rc;
+    if (v && (rc = check_rows(v, dtype, batch->n_rows, "v", &a.v)) != KVS_OK) return rc;
     OnDevice on;
     if ((rc = on.enter(pool->pages)) != KVS_OK) return rc;
     if (a.batch.n_rows == 0 || a.batch.n_seqs == 0) return KVS_OK;
@@ -216,7 +217,7 @@ extern "C" int kvs_attend_pages(const kvs_page_pool* pool, const kvs_page_batch*
     if (n_q_heads < 1 || n_q_heads % a.pool.n_kv) return fail(KVS_E_INVAL, "n_q_heads must be a positive multiple of n_kv_heads");
     if (q_dtype != KVS_DT_F16 && q_dtype != KVS_DT_BF16) return fail(KVS_E_INVAL, "q is F16 or BF16");
     if (!dtype_ok(out_dtype)) return fail(KVS_E_INVAL, "unknown out_dtype");
-    if ((rc = check_rows(q, q_dtype, "q", &a.q)) != KVS_OK || (rc = check_rows(out, out_dtype, "out", &a.out)) != KVS_OK) return rc;
+    if ((rc = check_rows(q, q_dtype, batch->n_rows, "q", &a.q)) != KVS_OK || (rc = check_rows(out, out_dtype, batch->n_rows, "out", &a.out)) != KVS_OK) return rc;
     if (!aligned(lse, 4)) return fail(KVS_E_INVAL, "lse must be 4-byte aligned");
     a.n_qh = n_q_heads;
     a.group = n_q_heads / a.pool.n_kv;

@@ -481,7 +481,7 @@ typedef struct kvs_page_batch {
 
 /* A [n_rows][heads][128] tensor of KVS_DT_* values with its strides, in
  * values; the 128 values of a head are contiguous.  Address and strides must
- * be multiples of 16 bytes. */
+ * be multiples of 16 bytes.  The address may be NULL where n_rows is 0. */
 typedef struct kvs_page_rows {
     void* data;
     long long row_stride, head_stride;

@@ -54,3 +54,17 @@ def test_a_short_sequence_replayed_where_a_long_one_was_captured():
         g.replay()
         t.cuda.synchronize()
         check(b, q.double().cpu().numpy(), out, lse, wide=True)
+
+
+def test_batches_without_rows():
+    """Tensors of no rows (null addresses) are the smallest batch: nothing is done."""
+    t = torch()
+    b = Batch([0, 0], [300, 0], 4, 2, (Q8_0, Q4_0), prefix=40, seed=64).device(status=True)
+    before = b.d_pool.clone()
+    kv, q = t.empty(0, 2, 128, dtype=t.float16, device="cuda"), t.empty(0, 4, 128, dtype=t.float16, device="cuda")
+    f = t.ones(64, device="cuda")
+    b.kvs.kvs_append_pages(b.c_pool, b.c_batch, kv, kv, q, t.empty_like(q), b.kvs.make_rope(f))
+    b.kvs.kvs_read_pages(b.c_pool, b.c_batch, kv, t.empty_like(kv))
+    b.kvs.kvs_attend_pages(b.c_pool, b.c_batch, q, t.empty_like(q), t.empty(0, 4, device="cuda"), None, b.c_prefix, b.workspace())
+    t.cuda.synchronize()
+    assert t.equal(b.d_pool, before) and int(b.status) == 0
