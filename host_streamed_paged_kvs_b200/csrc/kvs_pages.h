@@ -168,8 +168,11 @@ struct RowView {
 __device__ __forceinline__ RowView row_view(const AttendPagesArgs& a, int seq, int row) {
     RowView v;
     const int len = max(a.batch.seq_len[seq], 0);
-    v.pos = a.prefix_len + a.batch.seq_len[seq] - (a.batch.q_start[seq + 1] - row);
-    v.first = a.first_key ? a.first_key[row] : (a.window > 0 ? v.pos - a.window + 1 : 0);
+    // in 64 bits: a length near 2^31 behind a prefix and the largest window before
+    // position -1 pass int32 (such a length is beyond any page table and ends as bad)
+    const long long pos = (long long)a.prefix_len + a.batch.seq_len[seq] - ((long long)a.batch.q_start[seq + 1] - row);
+    v.pos = (int)max(min(pos, 0x7ffffffell), -0x7fffffffll);
+    v.first = a.first_key ? a.first_key[row] : (a.window > 0 ? (int)max((long long)v.pos - a.window + 1, 0ll) : 0);
     v.end = a.end_key ? a.end_key[row] : v.pos + 1;
     v.first = max(v.first, 0);
     // 0 .. the keys that exist: callers subtract the prefix from it, which an end far below 0 would not survive

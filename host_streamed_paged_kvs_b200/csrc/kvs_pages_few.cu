@@ -179,7 +179,7 @@ __device__ __forceinline__ Seq seq_of(const AttendPagesArgs& a, int i) {
         keys = (int)min((long long)s.n_keys, most);
         s.stage0 = 0;
         if (a.window > 0 && !a.first_key)  // own keys before the first row's window are nobody's
-            s.stage0 = max(0, min(s.n_keys - s.rows - a.window + 1, keys - 1)) / kStageKeys;
+            s.stage0 = (int)max(0ll, min((long long)s.n_keys - s.rows - a.window + 1, (long long)keys - 1)) / kStageKeys;
     }
     s.n_groups = (int)(((long long)s.rows * a.group + ROWS - 1) / ROWS);
     s.n_stages = max(1, (keys + kStageKeys - 1) / kStageKeys - s.stage0);
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
             int st0 = s.stage0 + (int)(cur - unit0), st1 = s.stage0 + (int)(stop - unit0);
             if (lo < hi) {
                 st0 = max(st0, lo / kStageKeys);
-                st1 = min(st1, (hi + kStageKeys - 1) / kStageKeys);
+                st1 = min(st1, (hi - 1) / kStageKeys + 1);
             } else st1 = st0;
             if (lane < ROWS) {
                 p.token[lane] = token;

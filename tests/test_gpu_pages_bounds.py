@@ -68,3 +68,27 @@ def test_batches_without_rows():
     b.kvs.kvs_attend_pages(b.c_pool, b.c_batch, q, t.empty_like(q), t.empty(0, 4, device="cuda"), None, b.c_prefix, b.workspace())
     t.cuda.synchronize()
     assert t.equal(b.d_pool, before) and int(b.status) == 0
+
+
+@pytest.mark.parametrize("new", [6, 40], ids=["few-rows", "many-rows"])
+@pytest.mark.parametrize("prefix", [0, 20])
+def test_largest_window_at_negative_positions(new, prefix):
+    """Rows before position -1 whose end_key lies past them, with the largest window:
+    its lower bound is below int32."""
+    b = Batch([new], [3], 2, 1, (Q8_0, Q4_0), prefix=prefix, seed=62).device()
+    end = np.full(new, prefix + 3, np.int32)
+    score = b.kvs.make_score(window=2 ** 31 - 1, end_key=torch().from_numpy(end).cuda())
+    check(b, *run(b, "float16", "float32", score=score), wide=new > 16, window=2 ** 31 - 1, end=end)
+
+
+@pytest.mark.parametrize("new", [3, 40], ids=["few-rows", "many-rows"])
+@pytest.mark.parametrize("prefix", [0, 300])
+def test_largest_length(new, prefix):
+    """A length of 2^31 - 1, far beyond the table: NaN and the status bit, with a
+    prefix before it too."""
+    b = Batch([new, 1], [400, 100], 2, 1, (Q8_0, Q4_0), prefix=prefix, seed=63).device(status=True)
+    b.d["lens"][0] = 2 ** 31 - 1
+    q64, out, lse = run(b, "float16", "float32")
+    assert int(b.status) == b.kvs.KVS_ERR_BAD_PAGE
+    assert bool(out[:new].isnan().all()) and bool(lse[:new].isnan().all())
+    assert not bool(out[new:].isnan().any()) and not bool(lse[new:].isnan().any())
