@@ -44,6 +44,25 @@ __device__ __forceinline__ void store4(void* base, long long at, const float (&x
     }
 }
 
+// the same from 64 bits, each value rounded once (a value rounded to binary32 on
+// the way may fall on the middle of two numbers of the type)
+template <int DT>
+__device__ __forceinline__ void store4(void* base, long long at, const double (&x)[4]) {
+    if constexpr (DT == kDtF32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(base) + at) = make_float4((float)x[0], (float)x[1], (float)x[2], (float)x[3]);
+    } else {
+        uint2 v;
+        if constexpr (DT == kDtF16) {
+            *reinterpret_cast<__half2*>(&v.x) = __halves2half2(__double2half(x[0]), __double2half(x[1]));
+            *reinterpret_cast<__half2*>(&v.y) = __halves2half2(__double2half(x[2]), __double2half(x[3]));
+        } else {
+            *reinterpret_cast<__nv_bfloat162*>(&v.x) = __halves2bfloat162(__double2bfloat16(x[0]), __double2bfloat16(x[1]));
+            *reinterpret_cast<__nv_bfloat162*>(&v.y) = __halves2bfloat162(__double2bfloat16(x[2]), __double2bfloat16(x[3]));
+        }
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + at) = v;
+    }
+}
+
 __device__ __forceinline__ uint2 pack_half4(const float (&x)[4]) {
     uint2 v;
     *reinterpret_cast<__half2*>(&v.x) = __floats2half2_rn(x[0], x[1]);
@@ -231,8 +250,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_pages_kernel(const A
             s[u] = second ? cs[j].y : -cs[j].y;
         }
     }
-    auto rotate = [&](float (&x)[4]) {
-        if (a.rot == 0) return;  // uniform
+    auto rotate = [&](const float (&x)[4], double (&r)[4]) {
         float y[4];
         if (a.interleaved) {  // the lane's own other element
             y[0] = x[1]; y[1] = x[0]; y[2] = x[3]; y[3] = x[2];
@@ -252,8 +270,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_pages_kernel(const A
             }
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (4 * lane + u < a.rot) x[u] = (float)(c[u] * (double)x[u] + s[u] * (double)y[u]);
+        for (int u = 0; u < 4; ++u) r[u] = 4 * lane + u < a.rot ? c[u] * (double)x[u] + s[u] * (double)y[u] : (double)x[u];
     };
 #pragma unroll 2
     for (int h = h0 + warp; h < h1; h += kAppendWarps) {
@@ -262,14 +279,23 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_pages_kernel(const A
             float v[4];
             load4<DT>(a.k.p, row * a.k.row + h * a.k.head + 4 * lane, x);
             load4<DT>(a.v.p, row * a.v.row + h * a.v.head + 4 * lane, v);
-            rotate(x);
+            if (a.rot) {  // uniform
+                double r[4];
+                rotate(x, r);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) x[u] = (float)r[u];
+            }
             uint8_t* ph = a.pool.pages + ((size_t)max(page, 0) * n_kv + h) * G::kHeadBytes;
             store_kv<VT, KT>(ph, own_pos & 255, x, v, page >= 0);
         } else {
             const int qh = h - n_kv;
             load4<DT>(a.q.p, row * a.q.row + qh * a.q.head + 4 * lane, x);
-            rotate(x);
-            store4<DT>(a.q_out.p, row * a.q_out.row + qh * a.q_out.head + 4 * lane, x);
+            const long long to = row * a.q_out.row + qh * a.q_out.head + 4 * lane;
+            if (a.rot) {
+                double r[4];
+                rotate(x, r);
+                store4<DT>(a.q_out.p, to, r);
+            } else store4<DT>(a.q_out.p, to, x);
         }
     }
 }
