@@ -105,11 +105,13 @@ class kvs_eject_state(ctypes.Structure):
 
 
 class kvs_page_pool(ctypes.Structure):
+    device = None  # of its tensors, where make_* made it
     _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
                 ("type_k", ctypes.c_int), ("type_v", ctypes.c_int)]
 
 
 class kvs_page_batch(ctypes.Structure):
+    device = None  # of its tensors, where make_* made it
     _fields_ = [("n_seqs", ctypes.c_int), ("n_rows", ctypes.c_int), ("max_new", ctypes.c_int),
                 ("q_start", ctypes.c_void_p), ("seq_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
                 ("table_stride", ctypes.c_int), ("status", ctypes.c_void_p)]
@@ -120,16 +122,19 @@ class kvs_page_rows(ctypes.Structure):
 
 
 class kvs_rope(ctypes.Structure):
+    device = None  # of its tensors, where make_* made it
     _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
                 ("positions", ctypes.c_void_p), ("pos_offset", ctypes.c_int), ("mscale", ctypes.c_float)]
 
 
 class kvs_score(ctypes.Structure):
+    device = None  # of its tensors, where make_* made it
     _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int),
                 ("alibi_slopes", ctypes.c_void_p), ("first_key", ctypes.c_void_p), ("end_key", ctypes.c_void_p)]
 
 
 class kvs_page_prefix(ctypes.Structure):
+    device = None  # of its tensors, where make_* made it
     _fields_ = [("page_table", ctypes.c_void_p), ("n_tokens", ctypes.c_int)]
 
 
@@ -404,6 +409,21 @@ def _float32(x, what: str, least: int) -> Optional[int]:
     return x.data_ptr()
 
 
+def _device(what: str, *tensors) -> Optional[int]:
+    """The one device of the tensors given (None: none is)."""
+    at = {x.get_device() for x in tensors if x is not None}
+    if len(at) > 1:
+        _bad(f"{what}: tensors of one device are wanted")
+    return at.pop() if at else None
+
+
+def _beside(pool, d) -> None:
+    """Refuses a descriptor whose tensors are not on the pool's device (structs filled from
+    addresses have none)."""
+    if None not in (pool.device, d.device):
+        _bad(f"{type(d).__name__}: its tensors must be on the pool's device")
+
+
 def make_page_pool(pages, n_kv_heads: int, type_k: int = KVS_TYPE_Q8_0, type_v: int = KVS_TYPE_Q4_0) -> kvs_page_pool:
     """A pool of pages: a contiguous uint8 device tensor of whole pages."""
     head = kvs_page_bytes(make_config(1, n_kv_heads, n_kv_heads, 256, 1, type_k=type_k, type_v=type_v))
@@ -413,6 +433,7 @@ def make_page_pool(pages, n_kv_heads: int, type_k: int = KVS_TYPE_Q8_0, type_v: 
         _bad(f"pages: a contiguous uint8 device tensor of whole pages of {head} bytes is wanted")
     p = kvs_page_pool(pages.data_ptr(), pages.numel() // head, n_kv_heads, type_k, type_v)
     p.keep = pages
+    p.device = pages.get_device()
     return p
 
 
@@ -424,6 +445,7 @@ def make_page_batch(q_start, seq_len, page_table, n_rows: int, max_new: int = 0,
     b = kvs_page_batch(n, n_rows, max_new, _int32(q_start, "q_start", n + 1), _int32(seq_len, "seq_len"),
                        _int32(page_table, "page_table"), page_table.shape[1], _int32(status, "status", 1))
     b.keep = (q_start, seq_len, page_table, status)
+    b.device = _device("page batch", *b.keep)
     return b
 
 
@@ -433,6 +455,7 @@ def make_rope(inv_freq, rot_dim: int = 128, interleaved: bool = False, positions
     r = kvs_rope(_float32(inv_freq, "inv_freq", rot_dim // 2), rot_dim, int(interleaved), _int32(positions, "positions"),
                  pos_offset, mscale)
     r.keep = (inv_freq, positions)
+    r.device = _device("rope", *r.keep)
     return r
 
 
@@ -442,6 +465,7 @@ def make_score(scale: float = 0.0, softcap: float = 0.0, window: int = 0, alibi_
     s = kvs_score(scale, softcap, window, _float32(alibi_slopes, "alibi_slopes", 1), _int32(first_key, "first_key"),
                   _int32(end_key, "end_key"))
     s.keep = (alibi_slopes, first_key, end_key)
+    s.device = _device("score", *s.keep)
     return s
 
 
@@ -449,17 +473,18 @@ def make_page_prefix(page_table, n_tokens: int) -> kvs_page_prefix:
     """page_table int32 [pages of n_tokens]."""
     p = kvs_page_prefix(_int32(page_table, "prefix page_table", -(-n_tokens // 256)), n_tokens)
     p.keep = page_table
+    p.device = _device("page prefix", page_table)
     return p
 
 
-def _rows(x, batch, heads: int, what: str):
-    """(descriptor, dtype code) of a [rows, heads, 128] device tensor, strides as they are."""
+def _rows(x, batch, heads: int, what: str, at: Optional[int]):
+    """(descriptor, dtype code) of a [rows, heads, 128] tensor on device `at`, strides as they are."""
     dt = _dtype(x)
-    shape, stride = x.shape, x.stride()
+    shape, stride, on = x.shape, x.stride(), x.get_device()
     if dt is None or len(shape) != 3 or shape[0] < batch.n_rows or shape[1] != heads or shape[2] != 128 or \
-            stride[2] != 1 or not x.is_cuda:
-        _bad(f"{what}: a float16, bfloat16 or float32 device tensor [rows >= {batch.n_rows}, {heads}, 128] with "
-             "contiguous heads is wanted")
+            stride[2] != 1 or on < 0 or (on != at and at is not None):
+        _bad(f"{what}: a float16, bfloat16 or float32 tensor [rows >= {batch.n_rows}, {heads}, 128] with "
+             "contiguous heads on the pool's device is wanted")
     return kvs_page_rows(x.data_ptr(), stride[0], stride[1]), dt
 
 
@@ -471,8 +496,13 @@ def _same(a: int, b: int, what: str) -> int:
 
 def kvs_append_pages(pool, batch, k, v, q=None, q_out=None, rope=None, stream=None) -> None:
     """Rotate K (and Q into q_out), quantize K and V and write them to the batch's pages."""
-    kr, dt = _rows(k, batch, pool.n_kv_heads, "k")
-    vr, dv = _rows(v, batch, pool.n_kv_heads, "v")
+    at = pool.device
+    if batch.device != at:
+        _beside(pool, batch)
+    if rope is not None and rope.device != at:
+        _beside(pool, rope)
+    kr, dt = _rows(k, batch, pool.n_kv_heads, "k", at)
+    vr, dv = _rows(v, batch, pool.n_kv_heads, "v", at)
     _same(dt, dv, "k and v")
     qr = qo = None
     heads = 0
@@ -480,7 +510,7 @@ def kvs_append_pages(pool, batch, k, v, q=None, q_out=None, rope=None, stream=No
         if q is None or q_out is None or q.dim() != 3:
             _bad("q and q_out go together, [rows, heads, 128]")
         heads = q.shape[1]
-        (qr, d0), (qo, d1) = _rows(q, batch, heads, "q"), _rows(q_out, batch, heads, "q_out")
+        (qr, d0), (qo, d1) = _rows(q, batch, heads, "q", at), _rows(q_out, batch, heads, "q_out", at)
         _same(_same(dt, d0, "k and q"), d1, "k and q_out")
     if rope is not None and rope.keep[1] is not None and rope.keep[1].numel() < batch.n_rows:
         _bad("positions: one per row is wanted")
@@ -489,8 +519,11 @@ def kvs_append_pages(pool, batch, k, v, q=None, q_out=None, rope=None, stream=No
 
 def kvs_read_pages(pool, batch, k=None, v=None, stream=None) -> None:
     """Write the values of the batch's rows, read from its pages, to k and / or v."""
-    kr, dk = _rows(k, batch, pool.n_kv_heads, "k") if k is not None else (None, None)
-    vr, dv = _rows(v, batch, pool.n_kv_heads, "v") if v is not None else (None, None)
+    at = pool.device
+    if batch.device != at:
+        _beside(pool, batch)
+    kr, dk = _rows(k, batch, pool.n_kv_heads, "k", at) if k is not None else (None, None)
+    vr, dv = _rows(v, batch, pool.n_kv_heads, "v", at) if v is not None else (None, None)
     if dk is None and dv is None:
         _bad("neither k nor v is wanted")
     dt = _same(dk, dv, "k and v") if dk is not None and dv is not None else (dk if dv is None else dv)
@@ -510,11 +543,17 @@ def kvs_attend_pages(pool, batch, q, out, lse=None, score=None, prefix=None, wor
     if q.dim() != 3:
         _bad("q: [rows, heads, 128] is wanted")
     heads = q.shape[1]
-    (qr, dq), (orow, do) = _rows(q, batch, heads, "q"), _rows(out, batch, heads, "out")
-    if workspace is None:
-        _bad("a workspace is wanted (kvs_attend_pages_workspace bytes, zero-filled)")
-    if lse is not None and (_dtype(lse) != KVS_DT_F32 or not lse.is_contiguous() or lse.numel() < batch.n_rows * heads):
-        _bad("lse: a contiguous float32 tensor [n_rows, heads] is wanted")
+    at = pool.device
+    for d in (batch, score, prefix):
+        if d is not None and d.device != at:
+            _beside(pool, d)
+    (qr, dq), (orow, do) = _rows(q, batch, heads, "q", at), _rows(out, batch, heads, "out", at)
+    qat = q.get_device()  # the pool's, where that is known
+    if workspace is None or workspace.get_device() != qat or not workspace.is_contiguous():
+        _bad("a workspace is wanted (kvs_attend_pages_workspace bytes, zero-filled, contiguous, on the pool's device)")
+    if lse is not None and (_dtype(lse) != KVS_DT_F32 or not lse.is_contiguous() or lse.numel() < batch.n_rows * heads or
+                            lse.get_device() != qat):
+        _bad("lse: a contiguous float32 tensor [n_rows, heads] on the pool's device is wanted")
     if score is not None:
         slopes, first, end = score.keep
         if (slopes is not None and slopes.numel() < heads) or any(x is not None and x.numel() < batch.n_rows
@@ -522,7 +561,6 @@ def kvs_attend_pages(pool, batch, q, out, lse=None, score=None, prefix=None, wor
             _bad("score: alibi_slopes has one value a head, first_key and end_key one a row")
     _check(lib.kvs_attend_pages(pool, batch, dq, heads, qr, do, orow, _addr(lse), score, prefix, workspace.data_ptr(),
                                 workspace.numel() * workspace.element_size(), _stream(stream)))
-
 
 
 def kvs_selftest_bounded_wait(device: int = 0, limit_s: float = 0.2) -> int:
