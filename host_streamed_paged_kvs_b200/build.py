@@ -11,7 +11,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libkvs.so")
 SOURCES = ["kvs_kernels.cu", "kvs_chunk_mma.cu", "kvs_runtime.cpp", "kvs_static.cu",
            "kvs_pages.cpp", "kvs_pages.cu", "kvs_pages_few.cu", "kvs_pages_wide.cu"]
-HEADERS = ["kvs_internal.h", "kvs_ptx.cuh", "kvs_pages.h", "kvs_pages_finish.cuh"]
+HEADERS = ["kvs_internal.h", "kvs_ptx.cuh", "kvs_pages.h", "kvs_pages_finish.cuh", "kvs_pages_wait.h"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 

@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
     uint64_t* p_full = p_meta + kSlots;                               // [piece slot] rows and Q too
     uint64_t* p_empty = p_full + kSlots;                              // [piece slot] consumers and loader done
     int* sLast = reinterpret_cast<int*>(p_empty + kSlots);            // this CTA joins the unit
+    int* sSlow = sLast + 1;                                           // warps that recompute a row
     float* sml = reinterpret_cast<float*>(p_empty + kSlots + 2);      // [warp][8][2] (reference, sum)
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -218,6 +219,7 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
     const int n_seqs = a.prefix_phase ? 1 : a.batch.n_seqs;
 
     if (tid == 0) {
+        *sSlow = 0;
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], kConsumers);
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                 if (seq < n_seqs) s = seq_of<ROWS>(a, seq);
             }
             Piece<ROWS>& p = pieces[slot];
-            ok = __all_sync(0xffffffffu, wait_phase(&p_empty[slot], slot_phase, a.batch.status));
+            ok = __all_sync(0xffffffffu, wait_phase(&p_empty[slot], slot_phase, a.batch.status, sSlow));
             if (!ok || cur >= run1 || seq >= n_seqs) {
                 if (lane == 0) p.n_stages = -1;
                 __syncwarp();
@@ -434,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
         long long issued = 0;
         bool ok = true;
         for (;;) {
-            ok = __all_sync(0xffffffffu, wait_phase(&p_meta[slot], slot_phase, a.batch.status));
+            ok = __all_sync(0xffffffffu, wait_phase(&p_meta[slot], slot_phase, a.batch.status, sSlow));
             Piece<ROWS>& p = pieces[slot];
             if (!ok || p.n_stages < 0) break;
             const int st0 = p.first_stage, st1 = st0 + p.n_stages, h = p.kv_head;
@@ -448,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                     pages = j + lane < n_table ? table[j + lane] : -1;
                 }
                 int page = __shfl_sync(0xffffffffu, pages, j - pages_at);
-                ok = __all_sync(0xffffffffu, wait_phase(&empty[buf], buf_phase, a.batch.status));
+                ok = __all_sync(0xffffffffu, wait_phase(&empty[buf], buf_phase, a.batch.status, sSlow));
                 if (!ok) break;
                 if (lane == 0) {
                     if ((unsigned)page >= (unsigned)a.pool.n_pages) page = 0;  // some page: rows that see it come out as NaN
@@ -518,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
     uint32_t slot_phase = 0;
     for (;;) {
         Piece<ROWS>& p = pieces[slot];
-        ok = wait_phase(&p_full[slot], slot_phase, a.batch.status);
+        ok = wait_phase(&p_full[slot], slot_phase, a.batch.status, sSlow);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok || p.n_stages < 0) {
             consumers_sync();
@@ -542,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
         const uint8_t* sq = p.q + g * kQRow + 8 * q;  // this lane's operand: row g, dims 16 c + 4 q ..
         const int n_stages = p.n_stages;
         for (int i = 0; i < n_stages; ++i) {
-            ok = wait_phase(&full[buf], buf_phase, a.batch.status);
+            ok = wait_phase(&full[buf], buf_phase, a.batch.status, sSlow);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const uint8_t* sb = smem + buf * G::kBytes;
@@ -881,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, Geo<VT, KT, NT>::kPerSm)
                          sml[(w * 8 + r) * 2 + 1]);
                 if (!record) {
                     join(acc, M, L, pacc[rr], pml[rr].x, pml[rr].y);
-                    end_row<VT, KT>(a, p.seq, p.token[pr], p.head[pr], acc, M, L);
+                    end_row<VT, KT>(a, p.seq, p.token[pr], p.head[pr], acc, M, L, sSlow);
                 } else {
                     float* rec = a.records + ((size_t)(blockIdx.x * 2 + p.slot) * kFewRowsMax + pr) * kRecordFloats;
                     *reinterpret_cast<float4*>(rec + 4 * lane) = acc;

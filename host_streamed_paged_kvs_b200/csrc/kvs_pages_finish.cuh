@@ -7,25 +7,22 @@
 #include <math_constants.h>
 
 #include "kvs_pages.h"
+#include "kvs_pages_wait.h"
 #include "kvs_ptx.cuh"
 
 namespace kvs {
 
-// Waits for an mbarrier phase, for at most about 10 s (rows may be recomputed the
-// slow way meanwhile).  The clock is read only after many failed tries: reading
-// it costs more than the wait for a barrier that is nearly always complete.
-constexpr uint64_t kPagesWaitNs = 10000000000ull;
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int* err) {
-    uint64_t t0 = 0;
+// Waits for an mbarrier phase, for at most about 10 s beside the time that other
+// warps of the block take to recompute rows (*busy counts them).  The clock is
+// read only after many failed tries: reading it costs more than the wait for a
+// barrier that is nearly always complete.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int* err, const volatile int* busy) {
+    WaitClock clock;
     for (uint32_t it = 0;; ++it) {
         if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 1023) == 1023) {
-            const uint64_t t = globaltimer_ns();
-            if (t0 == 0) t0 = t;
-            else if (t - t0 > kPagesWaitNs) {
-                if (err) atomicOr(err, kErrWaitTimeout);
-                return false;
-            }
+        if ((it & 1023) == 1023 && clock.expired(globaltimer_ns(), *busy != 0)) {
+            if (err) atomicOr(err, kErrWaitTimeout);
+            return false;
         }
     }
 }
@@ -81,11 +78,13 @@ __device__ __forceinline__ float one_value(const void* p, long long at) {
 // infinity or NaN is NaN; products of weights and scales may also pass fp16's
 // range.  Rows that end non-finite with a finite sum of weights come here, so
 // that what they do not see does not count.  Slow (a few us per 32 keys), and
-// no call with finite, moderate values reaches it.
+// no call with finite, moderate values reaches it.  busy: counts the block's warps
+// that are here, for those that wait; null where none does.
 template <int VT, int KT>
-__device__ __noinline__ float4 slow_row(const AttendPagesArgs& a, int seq, int row, int head) {
+__device__ __noinline__ float4 slow_row(const AttendPagesArgs& a, int seq, int row, int head, int* busy) {
     using G = PageGeom<VT, KT>;
     const int lane = threadIdx.x & 31, h = head / a.group;
+    if (busy && lane == 0) atomicAdd(busy, 1);
     const RowView v = row_view(a, seq, row);
     const float slope = a.slopes ? a.slopes[head] : 0.0f;
     auto head_of = [&](int key) -> const uint8_t* {
@@ -132,6 +131,7 @@ __device__ __noinline__ float4 slow_row(const AttendPagesArgs& a, int seq, int r
 #pragma unroll
     for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
     const float r = 1.0f / l;
+    if (busy && lane == 0) atomicAdd(busy, -1);
     return make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
 }
 
@@ -171,9 +171,9 @@ __device__ __forceinline__ void join(float4& acc, float& M, float& L, const floa
 // The end of one row, by a whole warp: lane holds sums of dims 4 lane .. + 3
 // relative to 2^M, L the sum of weights (0: the row sees nothing), the prefix's
 // part joined.  The prefix phase keeps the record, the own phase divides and
-// writes.
+// writes.  busy as for slow_row.
 template <int VT, int KT>
-__device__ __forceinline__ void end_row(const AttendPagesArgs& a, int seq, int row, int head, const float4& acc, float M, float L) {
+__device__ __forceinline__ void end_row(const AttendPagesArgs& a, int seq, int row, int head, const float4& acc, float M, float L, int* busy) {
     const int lane = threadIdx.x & 31;
     const size_t at = (size_t)row * a.n_qh + head;
     if (a.prefix_phase) {
@@ -187,7 +187,7 @@ __device__ __forceinline__ void end_row(const AttendPagesArgs& a, int seq, int r
         o = make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r);
         // inf - inf and 0 * inf make NaN, so a sum that is finite times 0 is 0
         const bool bad = !((acc.x + acc.y + acc.z + acc.w) * 0.0f == 0.0f);
-        if (__any_sync(0xffffffffu, bad) && L * 0.0f == 0.0f) o = slow_row<VT, KT>(a, seq, row, head);
+        if (__any_sync(0xffffffffu, bad) && L * 0.0f == 0.0f) o = slow_row<VT, KT>(a, seq, row, head, busy);
     }
     store_out4(a, row, head, 4 * lane, o);
     if (a.lse && lane == 0) a.lse[at] = L == 0.0f ? -CUDART_INF_F : (M + log2f(L)) * 0.69314718055994531f;
@@ -201,7 +201,7 @@ __device__ __forceinline__ void finish_row(const AttendPagesArgs& a, int seq, in
         const float2 ml = a.prior_ml[at];
         join(acc, M, L, reinterpret_cast<const float4*>(a.prior_acc)[at * 32 + (threadIdx.x & 31)], ml.x, ml.y);
     }
-    end_row<VT, KT>(a, seq, row, head, acc, M, L);
+    end_row<VT, KT>(a, seq, row, head, acc, M, L, nullptr);
 }
 
 }  // namespace kvs

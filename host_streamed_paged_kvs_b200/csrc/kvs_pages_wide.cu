@@ -361,6 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 25);
     int* sGroup = reinterpret_cast<int*>(tmem_slot + 1);
     volatile int* sAbort = reinterpret_cast<volatile int*>(sGroup + 1);
+    int* sSlow = sGroup + 2;        // warps that recompute rows
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n_kv = a.pool.n_kv;
@@ -370,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (tid == 32) {
         *sAbort = 0;
+        *sSlow = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&k_full[i], KT == kKF16 ? 1 : kKWarps);
             mbar_init(&k_free[i], 1);
@@ -401,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {  // by one thread or a whole warp
         if (ok && mbar_try_wait(bar, parity)) return true;
         if (!ok || *sAbort) return ok = false;
-        if (!wait_phase(bar, parity, a.batch.status)) {
+        if (!wait_phase(bar, parity, a.batch.status, sSlow)) {
             ok = false;
             *sAbort = 1;
         }
@@ -703,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int row = __ffs(redo) - 1;
                 const int tk = __shfl_sync(0xffffffffu, token, row), hd = __shfl_sync(0xffffffffu, head, row);
                 const int sq_ = __shfl_sync(0xffffffffu, seq, row);
-                store_out4(a, tk, hd, 4 * lane, slow_row<VT, KT>(a, sq_, tk, hd));
+                store_out4(a, tk, hd, 4 * lane, slow_row<VT, KT>(a, sq_, tk, hd, sSlow));
             }
             // any row of the warp: a row that ends beyond the table may be in any lane
             if (__any_sync(0xffffffffu, bad) && lane == 0 && a.batch.status) atomicOr(a.batch.status, kErrBadPage);
@@ -981,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (run0 < run1) {  // nothing is in flight when the memory is given back
             commit_one(done, one);
-            wait_phase(done, 0, a.batch.status);
+            wait_phase(done, 0, a.batch.status, sSlow);
         }
         __syncwarp();
     }
