@@ -7,8 +7,8 @@
 // What bounds it: HBM.  A key costs 208 B per kv head (K Q8_0 / V Q4_0) and is
 // read once for all rows of its kv head; at 6.5 TB/s an SM has 9 cycles per
 // key for everything else, and the math below takes 23 warp instructions.
-// Measured: one 256K sequence with 40 / 8 heads 99 us, 4.4 TB/s (the copies
-// alone 84 us); 64 sequences of up to 8K, 32 / 8 heads, 126 us, 3.6 TB/s; one 4K
+// Measured: one 256K sequence with 40 / 8 heads 98 us, 4.4 TB/s (the copies
+// alone 84 us); 64 sequences of up to 8K, 32 / 8 heads, 122 us, 3.7 TB/s; one 4K
 // sequence 12 us, all of it latency.
 //
 // Work split.  A unit is (sequence, kv head, up to 8 NT rows); its keys come

@@ -6,7 +6,8 @@
 // rows against 128 keys are 16.8 MFLOP, 2,050 cycles of an SM at the dense rate
 // (2,400 at the rate that N = 128 instructions reach), beside 2,050 cycles of
 // exponentials (16 a cycle) and the conversion of 32,768 codes.  Measured: 4,280
-// cycles a stage; 256 query tokens at 64K with 40 / 8 heads 429 us, 800 TFLOP/s.
+// cycles a stage at 1.66 GHz, and about 20,000 a unit beside its stages; 256 query
+// tokens at 64K with 40 / 8 heads 429 us, 800 TFLOP/s.
 //
 // A unit is (row group of 256 rows, kv head): two 128-row tiles that share every
 // converted stage of 128 keys.  A planning launch finds each group's stages
@@ -147,9 +148,11 @@ __device__ __forceinline__ void st_chunk(uint8_t* tile, int row, int c, uint4 v)
 
 // ---- planning: the groups and the stages that their rows need ----
 // A unit's length in the list: its stages, then kUnitCost places without one,
-// for what a unit costs beside its stages (Q, the end of its rows: 12 us, about
-// five stages).  Without them a CTA got 14 one-stage units of packed documents
-// while others got one unit of 14 stages: 379 us instead of 208.
+// for what a unit costs beside its stages (Q, the end of its rows).  Without them
+// a CTA got 14 one-stage units of packed documents while others got one unit of
+// 14 stages.  4,096 packed tokens at 0, 2, 3, 4, 5, 6, 8 places: 367, 207, 204,
+// 209, 213, 223, 231 us; 64 sequences on a 32K prefix 163, 158, 155, 154, 154, 155,
+// 155; 256 tokens at 64K 428 to 438 whatever it is.
 constexpr int kUnitCost = 4;
 __device__ __forceinline__ long long span_of(const WideUnit& u) { return u.n_stages + kUnitCost; }
 

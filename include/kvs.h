@@ -420,10 +420,12 @@ int kvs_attend_pages_static(const void* pages, int n_pages, int n_tokens, int n_
  * pages live in one caller-owned device pool and are found through page
  * tables: what a serving engine with its own page allocator needs beside the
  * handle calls above (whose pool streams from host memory).  No handle, no
- * allocation; every call is one to three kernels on `stream`, can be captured
- * into a CUDA graph, and reads the batch (row ranges, lengths, page tables)
- * from device memory when it runs, so a captured graph can be replayed after
- * those arrays, or the tensors' contents, have changed.
+ * allocation; a call is a few kernels on `stream` (append and read one;
+ * attention one for few rows, three for many, four for both, and one or three
+ * more for a shared prefix), can be captured into a CUDA graph, and reads the
+ * batch (row ranges, lengths, page tables) from device memory when it runs, so
+ * a captured graph can be replayed after those arrays, or the tensors'
+ * contents, have changed.
  *
  * The calls check what the host can see and return KVS_E_INVAL: null or
  * misaligned pointers, negative sizes, unsupported types, strides that the
@@ -461,7 +463,7 @@ typedef struct kvs_page_pool {
  * outside every sequence's range (padding) get nothing written.
  * q_start does not decrease.  Sequences may have no rows and no tokens.  More
  * rows than tokens is allowed: rows at negative positions append nothing, and
- * see nothing of their own pages. */
+ * see nothing of their own pages (but where an end_key says so). */
 typedef struct kvs_page_batch {
     int n_seqs;            /* >= 0 */
     int n_rows;            /* rows of the tensors; a bound on q_start[n_seqs] */
@@ -490,7 +492,8 @@ typedef struct kvs_page_rows {
 /* Rotary position embedding of K (and Q) rows: the pair (x0, x1) j of a head
  * becomes (x0 c - x1 s, x1 c + x0 s), c = mscale cos(a), s = mscale sin(a),
  * a = position * inv_freq[j], with the angle, its cosine and sine and the
- * rotation in 64 bits and one rounding at the end. */
+ * rotation in 64 bits and one rounding at the end (K to binary32, Q to its
+ * type). */
 typedef struct kvs_rope {
     const float* inv_freq; /* device [rot_dim / 2] */
     int rot_dim;           /* even, 0..128; values from rot_dim on are kept as they are;
@@ -510,7 +513,8 @@ typedef struct kvs_rope {
  * upper, which makes document masks (first = the document's first key) and
  * prefix masks (end past p + 1 inside a bidirectional part).  A row that sees
  * no key gets out = 0 and lse = -inf.  Values of keys that a row does not see
- * never count, whatever they hold. */
+ * never count, whatever they hold.  tanh is off by at most 4e-7, so a capped
+ * score by 4e-7 of its cap. */
 typedef struct kvs_score {
     float scale;               /* 0 = 1/sqrt(128) */
     float softcap;             /* 0 = none; > 0 */
@@ -549,20 +553,28 @@ int kvs_read_pages(const kvs_page_pool* pool, const kvs_page_batch* batch, int d
  * prefix if one is given.  q: q_dtype (F16 or BF16) [n_rows][n_q_heads][128];
  * out: out_dtype (F16, BF16 or F32); lse fp32 [n_rows][n_q_heads] (natural
  * log) or NULL; score and prefix may be NULL.  Products have 16-bit operands
- * and fp32 accumulation, softmax statistics are fp32.  Up to 32 rows per kv
- * head (rows of a sequence x n_q_heads / n_kv_heads) the probabilities go in
- * as two 16-bit terms unless out is BF16, so that an F32 or F16 result has
- * fp32-class accuracy with every V type but Q4_1 and Q5_1 (whose values are
- * rounded to fp16); wider rows use the tcgen05 tensor cores with K, V and
- * probabilities rounded to fp16 once each (a K value beyond fp16's range, which
- * only bf16 or fp32 input can bring, makes the rows that see it NaN there).
+ * and fp32 accumulation, softmax statistics are fp32; bf16 q goes in as fp16
+ * after a power of two per row (exact down to 2^-24 of the row's largest
+ * value).
+ *
+ * How many bits weights, K and V keep goes by the rows per kv head (rows x
+ * n_q_heads / n_kv_heads): of each sequence for its own pages, of the whole
+ * tensors (n_rows) for a shared prefix, whose pages all rows share.  Up to 32
+ * the weights go in as two 16-bit terms unless out is BF16, so that an F32 or
+ * F16 result has fp32-class accuracy with every V type but Q4_1 and Q5_1
+ * (whose values are rounded to fp16).  More go to the tcgen05 tensor cores
+ * with K, V and weights rounded to fp16 once each, whatever out is (a K value
+ * beyond fp16's range, which only bf16 or fp32 input can bring, makes the rows
+ * that see it NaN there).  A caller who wants fp32-class results of many short
+ * sequences behind a prefix of whole pages puts those into each page table
+ * instead.
  * out must not overlap q.  q_start, lengths and tables may change between
  * replays of a captured call, the batch's bounds (n_seqs, n_rows, max_new) and
  * addresses may not.
  *
  * workspace: device, 256-byte aligned, at least kvs_attend_pages_workspace
- * bytes, zero-filled once before its first use; every call leaves it ready for
- * the next.  Calls that share a workspace must be ordered (one stream, or
+ * bytes (that covers a prefix: 520 bytes a row and q head), zero-filled once
+ * before its first use; every call leaves it ready for the next.  Calls that share a workspace must be ordered (one stream, or
  * events): two calls at once, or two captured graphs replayed at once, need a
  * workspace each. */
 int kvs_attend_pages(const kvs_page_pool* pool, const kvs_page_batch* batch, int q_dtype, int n_q_heads,
